@@ -285,6 +285,235 @@ LI_API li_status li_sparse_attention(const li_sfa_params *p, const void *query, 
                                      const int32_t *block_table, void *out, float *lse,
                                      int32_t *status, void *stream);
 
+/*
+ * Rotary positions for the query and key heads that the indexer and the
+ * attention read.  Pair p (0 <= p < rot_dim/2) of row r turns by the angle
+ * a = positions[r] * inv_freq[p]:
+ *
+ *     y0 = mscale * (x0 cos a - x1 sin a)
+ *     y1 = mscale * (x1 cos a + x0 sin a)          (inverse: sin a -> -sin a)
+ *
+ * with x0, x1 at columns rot_offset + p and rot_offset + p + rot_dim/2 of the
+ * head (LI_ROPE_HALF) or rot_offset + 2p and rot_offset + 2p + 1
+ * (LI_ROPE_INTERLEAVED).  The other columns are copied.  `inverse` is the
+ * transposed turn: it undoes a call with the same mscale = 1, and for any
+ * mscale it takes an output's gradient to the input's.
+ *
+ *   dtype         LI_BF16, LI_FP16 or LI_FP32: query, key and outputs
+ *   rows          token rows (B*S1 or T1); 0 does nothing
+ *   N1, N2        query heads 1..1024; key heads 0..1024 (0: no key, key pointers NULL)
+ *   D             head dim 2..1024
+ *   rot_dim       even, 2..D; rot_offset >= 0; rot_offset + rot_dim <= D
+ *   mscale        finite, > 0 (1 when positions are not scaled)
+ *   *_stride      elements between consecutive rows / heads of query, key and
+ *                 the outputs (0 = dense: N*D and D), so that heads may lie in
+ *                 a wider projection; heads may not overlap (head stride >= D,
+ *                 row stride >= (N-1)*head stride + D)
+ *   reserved      must be 0
+ *   positions     device int32 [rows], any value
+ *   inv_freq      device fp64 [rot_dim/2], radians per position
+ *                 (li_rope_frequencies); the angle is reduced in 64 bits, so a
+ *                 far position costs no accuracy
+ * An output may be its input (same strides); otherwise outputs overlap
+ * nothing.  Pointers are aligned to their element; 16-byte alignment of
+ * everything (pointers, strides, D, rot_offset, and rot_dim/2 for
+ * LI_ROPE_HALF) is what the wide loads need.  One launch, no workspace.
+ */
+typedef enum { LI_ROPE_HALF = 0, LI_ROPE_INTERLEAVED = 1 } li_rope_pairing;
+typedef struct {
+    int32_t dtype;
+    int32_t rows, N1, N2, D;
+    int32_t rot_dim, rot_offset;
+    int32_t pairing, inverse;
+    float mscale;
+    int64_t q_row_stride, q_head_stride, k_row_stride, k_head_stride;
+    int64_t q_out_row_stride, q_out_head_stride, k_out_row_stride, k_out_head_stride;
+    int32_t reserved;
+} li_rope_params;
+
+LI_API li_status li_rope(const li_rope_params *p, const int32_t *positions, const double *inv_freq,
+                         const void *query, const void *key, void *query_out, void *key_out,
+                         void *stream);
+
+/*
+ * Host only: the radians per position of each pair, into inv_freq[rot_dim/2]
+ * (host memory), and the factor for li_rope_params.mscale.
+ *   LI_ROPE_SCALE_NONE    base^(-2p/rot_dim)
+ *   LI_ROPE_SCALE_LINEAR  the same / factor (positions interpolated)
+ *   LI_ROPE_SCALE_NTK     base replaced by base * factor^(rot_dim/(rot_dim-2))
+ *   LI_ROPE_SCALE_YARN    pairs that turn at least beta_fast times within
+ *                         original_positions are kept, those that turn at most
+ *                         beta_slow times are divided by factor, a linear ramp
+ *                         over p lies between; mscale = 0.1 ln(factor) + 1
+ * factor >= 1 (ignored by NONE); base > 1; rot_dim even, 2..1024 (NTK: >= 4);
+ * YARN needs original_positions >= 1 and beta_fast > beta_slow > 0.
+ */
+typedef enum { LI_ROPE_SCALE_NONE = 0, LI_ROPE_SCALE_LINEAR = 1, LI_ROPE_SCALE_NTK = 2, LI_ROPE_SCALE_YARN = 3 } li_rope_scaling;
+LI_API li_status li_rope_frequencies(int32_t scaling, int32_t rot_dim, double base, double factor,
+                                     int32_t original_positions, double beta_fast, double beta_slow,
+                                     double *inv_freq, float *mscale);
+
+/*
+ * The pages of a PA_BSND cache.  A cache is one or more pools (keys, values,
+ * scales, of any number of layers) whose axis 0 is the page ("block" in the
+ * calls that read them), a block_table [B, max_pages_per_seq], the lengths
+ * act_seq_k [B] and a reference count per page [num_pages] (0 = free); row b
+ * holds its pages in the first ceil(len_b / page_size) columns.  The calls
+ * below take this state (table, lens, refs) and write the new one to table_out,
+ * lens_out and refs_out, each of which is either its input (in place) or a
+ * buffer that overlaps nothing.  All decisions are taken on the device, in an
+ * order that does not depend on timing: free pages are handed out lowest page
+ * first, rows and pairs are served in the order of the arguments.
+ *
+ *   li_pages_reserve  grows row b to new_lens[b] tokens (a length that is not
+ *                     above the present one changes nothing)
+ *   li_pages_fork     makes the empty row dst_rows[i] a child of src_rows[i]:
+ *                     whole pages are shared (their count goes up), a partly
+ *                     filled last page is copied into a fresh one, so a page
+ *                     that is still written to has one owner
+ *   li_pages_free     empties rows: each of their pages' counts goes down, the
+ *                     row's columns become -1, its length 0
+ *   li_pages_compact  moves live pages down so that the n live pages are the
+ *                     pages 0 .. n-1: the i-th live page at or above n goes to
+ *                     the i-th free page below n; columns behind a row's pages
+ *                     become -1
+ *   li_pages_copy     copies page src[i] to page dst[i] of every pool; the
+ *                     destinations are distinct and no destination is a source
+ *                     of another pair (else their contents are undefined)
+ *
+ * When the free pages run out, the rows (pairs) from the first that no longer
+ * fits are left as they were and LI_DEV_NO_PAGES is flagged.  A row outside
+ * [0, B), a row named twice (the first counts), a fork onto a row that is not
+ * empty: skipped, LI_DEV_BAD_ROW.  A length outside [0, max_pages_per_seq *
+ * page_size]: the present length is clamped, a new one skipped,
+ * LI_DEV_BAD_KLEN.  A page number outside [0, num_pages), a page whose count
+ * would fall below 0: skipped (-1 in a written row), LI_DEV_BAD_BLOCK.
+ *
+ *   num_pages 1..2^26; page_size, max_pages_per_seq, B >= 1; max_pages_per_seq *
+ *   page_size and B * max_pages_per_seq <= 2^31-1
+ *   pools      host array of n_pools (0..256) descriptors: base (device), bytes
+ *              of one page, bytes between pages (>= page_bytes)
+ *   status     device int32 that receives LI_DEV_* bits by atomic OR, or NULL
+ *   workspace  device buffer of li_pages_workspace_size bytes, 256-byte
+ *              aligned, not shared by calls that may run at the same time
+ * Two launches (li_pages_copy: one; one more per 64 pools beyond the first 64).
+ */
+#define LI_DEV_NO_PAGES      0x40  /* pages: the free pages ran out (rows left as they were) */
+#define LI_DEV_BAD_ROW       0x80  /* pages: a row out of range, named twice, or not empty (skipped) */
+typedef struct {
+    int32_t num_pages, page_size, max_pages_per_seq, B;
+    int32_t reserved;
+} li_pages_params;
+typedef struct {
+    void *base;
+    int64_t page_bytes, page_stride;
+} li_page_pool;
+
+LI_API li_status li_pages_workspace_size(const li_pages_params *p, size_t *bytes);
+LI_API li_status li_pages_copy(const li_pages_params *p, const li_page_pool *pools, int32_t n_pools,
+                               const int32_t *src_pages, const int32_t *dst_pages, int32_t n,
+                               int32_t *status, void *stream);
+LI_API li_status li_pages_reserve(const li_pages_params *p, const int32_t *table, const int32_t *lens,
+                                  const int32_t *refs, const int32_t *new_lens, int32_t *table_out,
+                                  int32_t *lens_out, int32_t *refs_out, int32_t *status,
+                                  void *workspace, size_t workspace_bytes, void *stream);
+LI_API li_status li_pages_fork(const li_pages_params *p, const li_page_pool *pools, int32_t n_pools,
+                               const int32_t *table, const int32_t *lens, const int32_t *refs,
+                               const int32_t *src_rows, const int32_t *dst_rows, int32_t n,
+                               int32_t *table_out, int32_t *lens_out, int32_t *refs_out,
+                               int32_t *status, void *workspace, size_t workspace_bytes, void *stream);
+LI_API li_status li_pages_free(const li_pages_params *p, const int32_t *table, const int32_t *lens,
+                               const int32_t *refs, const int32_t *rows, int32_t n, int32_t *table_out,
+                               int32_t *lens_out, int32_t *refs_out, int32_t *status, void *workspace,
+                               size_t workspace_bytes, void *stream);
+LI_API li_status li_pages_compact(const li_pages_params *p, const li_page_pool *pools, int32_t n_pools,
+                                  const int32_t *table, const int32_t *lens, const int32_t *refs,
+                                  int32_t *table_out, int32_t *lens_out, int32_t *refs_out,
+                                  int32_t *status, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Segment-sparse attention: attention over the segments of seg_size
+ * consecutive keys that a cheap score selects for each query row and key head
+ * (the coarse sibling of li_indexer + li_sparse_attention: one score per
+ * segment instead of one per key, and any number of key heads).  With
+ * vis(r) the keys that row r sees (sparse_mode 0: Sk; 3: right-down causal,
+ * t <= i + Sk - Sq), ns(r) = ceil(vis(r) / seg_size) and n = the key head of
+ * query head h (heads n*G .. n*G+G-1, G = N1/N2):
+ *
+ *   li_segment_pool       P[b,s,n] = mean of key[t,n] over the keys t of
+ *                         segment s that lie below Sk
+ *   li_segment_select     score(r,n,s) = (sum of q[r,h] over the heads of n) . P[b,s,n],
+ *                         in 64 bits; the first init_segs and the last local_segs
+ *                         of the ns(r) segments are always selected, the best
+ *                         others fill the seg_count entries (ties: the lower
+ *                         segment; NaN counts as -inf).  Selected segments are
+ *                         written in ascending order, -1 behind them.
+ *   li_segment_attention  J = keys t < vis(r) of the selected segments;
+ *                         out_h = sum_J softmax(softmax_scale q_h . k_t) v_t,
+ *                         lse_h = log sum_J exp(softmax_scale q_h . k_t);
+ *                         0 and -inf when J is empty, and for BSND padding rows.
+ *                         What a row does not select has no effect on it, not
+ *                         even as a NaN or infinity.
+ *
+ *   layout_q, layout_kv   as li_sfa_params, with N2 key heads: key and value
+ *                         [B,S2,N2,D], [T2,N2,D] or [num_blocks,block_size,N2,D]
+ *   dtype                 LI_BF16 or LI_FP16: query, key, value, out
+ *   N1, N2, D             N2 divides N1, G = N1/N2 <= 128, N1 <= 1024; D (also
+ *                         the values' dim) 64 or 128
+ *   block_size            pages: a multiple of 16
+ *   kv_block_stride       elements between pages of the key pool and of the value
+ *                         pool (0 = dense); a multiple of 8
+ *   seg_size              a multiple of 16 in [16, 1024]
+ *   seg_count             entries per (row, key head), 1..1024
+ *   init_segs, local_segs >= 0, together <= seg_count; local_segs >= 1 with
+ *                         sparse_mode 3 (a segment that a row sees in part is
+ *                         then always selected and its mean, which looks ahead,
+ *                         is never used)
+ *   max_segs              segments per sequence of P: [B, max_segs, N2, D]
+ *                         fp32; 1..16384.  Longer sequences are cut there and
+ *                         flagged with LI_DEV_BAD_KLEN (pool and select only).
+ *   softmax_scale         > 0 and finite
+ *   reserved              must be 0
+ *
+ *   first      (pool) device int32 [B] or NULL: only the segments of tokens
+ *              first[b] .. Sk-1 are written, as after appending tokens;
+ *              segments before them and behind the last keep what they hold
+ *   pooled     device fp32, 16-byte aligned
+ *   seg_idx    int32 [rows, N2, seg_count]; attention takes ascending entries, -1
+ *              anywhere is skipped; an entry that is below -1, not below
+ *              ceil(Sk/seg_size), or not above the entries before it in its
+ *              row is skipped and flagged with LI_DEV_BAD_INDEX
+ *   out        [rows, N1, D] dtype; lse fp32 [rows, N1] or NULL
+ *   status     as in li_sparse_attention
+ * Pointers: query, key, value, out and pooled 16-byte aligned, the others
+ * 4-byte.  Accumulation is fp32; the softmax weights enter the P.V product
+ * rounded to dtype.  One launch each, no workspace.
+ */
+typedef struct {
+    int32_t layout_q, layout_kv;
+    int32_t dtype;
+    int32_t B, S1, S2, T1, T2;
+    int32_t N1, N2, D;
+    int32_t num_blocks, block_size, max_blocks_per_seq;
+    int64_t kv_block_stride;
+    int32_t seg_size, seg_count, init_segs, local_segs, max_segs;
+    int32_t sparse_mode;
+    float softmax_scale;
+    int32_t reserved;
+} li_segment_params;
+
+LI_API li_status li_segment_pool(const li_segment_params *p, const void *key, const int32_t *act_seq_k,
+                                 const int32_t *block_table, const int32_t *first, float *pooled,
+                                 int32_t *status, void *stream);
+LI_API li_status li_segment_select(const li_segment_params *p, const void *query, const float *pooled,
+                                   const int32_t *act_seq_q, const int32_t *act_seq_k, int32_t *seg_idx,
+                                   int32_t *status, void *stream);
+LI_API li_status li_segment_attention(const li_segment_params *p, const void *query, const void *key,
+                                      const void *value, const int32_t *seg_idx,
+                                      const int32_t *act_seq_q, const int32_t *act_seq_k,
+                                      const int32_t *block_table, void *out, float *lse,
+                                      int32_t *status, void *stream);
+
 /* Thread-local message describing the last non-OK status. */
 LI_API const char *li_last_error(void);
 

@@ -29,6 +29,9 @@ DTYPE = {"bf16": 0, "fp16": 1, "fp32": 2, "e4m3": 3, "int8": 4}
 LAYOUT = {"BSND": 0, "TND": 1, "PA_BSND": 2}
 DEV_BAD_QLEN, DEV_BAD_KLEN, DEV_BAD_BLOCK, DEV_NEG_SCALE, DEV_TIMEOUT = 1, 2, 4, 8, 16
 DEV_BAD_INDEX = 32
+DEV_NO_PAGES, DEV_BAD_ROW = 64, 128
+ROPE_PAIRING = {"half": 0, "interleaved": 1}
+ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 INT64_MAX = (1 << 63) - 1
 # LI_NOALLOC_SCRATCH_BYTES of include/li.h: the scratch li_indexer_noalloc holds
 NOALLOC_SCRATCH_BYTES = 32 << 20
@@ -36,7 +39,9 @@ NOALLOC_SCRATCH_BYTES = 32 << 20
 EXPORTS = ("li_output_shape", "li_workspace_size", "li_indexer", "li_quant_indexer", "li_topk",
            "li_last_error", "li_read_device_status", "li_selftest_bounded_wait",
            "li_last_launch_count", "li_set_profile_events", "li_indexer_noalloc",
-           "li_sparse_attention")
+           "li_sparse_attention", "li_rope", "li_rope_frequencies", "li_pages_workspace_size",
+           "li_pages_copy", "li_pages_reserve", "li_pages_fork", "li_pages_free", "li_pages_compact",
+           "li_segment_pool", "li_segment_select", "li_segment_attention")
 
 
 class LiError(RuntimeError):
@@ -79,6 +84,46 @@ class SfaParams(ctypes.Structure):
     ]
 
 
+class RopeParams(ctypes.Structure):
+    """Mirror of li_rope_params (rotary positions)."""
+    _fields_ = [
+        ("dtype", ctypes.c_int32), ("rows", ctypes.c_int32), ("N1", ctypes.c_int32), ("N2", ctypes.c_int32),
+        ("D", ctypes.c_int32), ("rot_dim", ctypes.c_int32), ("rot_offset", ctypes.c_int32),
+        ("pairing", ctypes.c_int32), ("inverse", ctypes.c_int32), ("mscale", ctypes.c_float),
+        ("q_row_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+        ("k_row_stride", ctypes.c_int64), ("k_head_stride", ctypes.c_int64),
+        ("q_out_row_stride", ctypes.c_int64), ("q_out_head_stride", ctypes.c_int64),
+        ("k_out_row_stride", ctypes.c_int64), ("k_out_head_stride", ctypes.c_int64),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+class PagesParams(ctypes.Structure):
+    """Mirror of li_pages_params (the pages of a cache)."""
+    _fields_ = [("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("max_pages_per_seq", ctypes.c_int32), ("B", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class PagePool(ctypes.Structure):
+    """Mirror of li_page_pool (one pool of a cache)."""
+    _fields_ = [("base", ctypes.c_void_p), ("page_bytes", ctypes.c_int64), ("page_stride", ctypes.c_int64)]
+
+
+class SegmentParams(ctypes.Structure):
+    """Mirror of li_segment_params (segment-sparse attention)."""
+    _fields_ = [
+        ("layout_q", ctypes.c_int32), ("layout_kv", ctypes.c_int32), ("dtype", ctypes.c_int32),
+        ("B", ctypes.c_int32), ("S1", ctypes.c_int32), ("S2", ctypes.c_int32),
+        ("T1", ctypes.c_int32), ("T2", ctypes.c_int32),
+        ("N1", ctypes.c_int32), ("N2", ctypes.c_int32), ("D", ctypes.c_int32),
+        ("num_blocks", ctypes.c_int32), ("block_size", ctypes.c_int32), ("max_blocks_per_seq", ctypes.c_int32),
+        ("kv_block_stride", ctypes.c_int64),
+        ("seg_size", ctypes.c_int32), ("seg_count", ctypes.c_int32), ("init_segs", ctypes.c_int32),
+        ("local_segs", ctypes.c_int32), ("max_segs", ctypes.c_int32), ("sparse_mode", ctypes.c_int32),
+        ("softmax_scale", ctypes.c_float), ("reserved", ctypes.c_int32),
+    ]
+
+
 _lib = None
 
 
@@ -91,6 +136,7 @@ def lib() -> ctypes.CDLL:
         L = ctypes.CDLL(LIB_PATH)
         vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
         P = ctypes.POINTER(Params)
+        G, L_, S_ = (ctypes.POINTER(t) for t in (PagesParams, PagePool, SegmentParams))
         sig = {
             "li_output_shape": (ctypes.c_int, [P, ctypes.POINTER(ctypes.c_int64), ctypes.POINTER(i32)]),
             "li_workspace_size": (ctypes.c_int, [P, ctypes.POINTER(sz)]),
@@ -105,6 +151,18 @@ def lib() -> ctypes.CDLL:
             "li_indexer_noalloc": (ctypes.c_int, [P, vp, vp, vp, vp, vp, vp, vp, vp, vp]),
             "li_sparse_attention": (ctypes.c_int, [ctypes.POINTER(SfaParams), vp, vp, vp, vp, vp,
                                                    vp, vp, vp, vp, vp, vp]),
+            "li_rope": (ctypes.c_int, [ctypes.POINTER(RopeParams)] + [vp] * 7),
+            "li_rope_frequencies": (ctypes.c_int, [i32, i32, ctypes.c_double, ctypes.c_double, i32, ctypes.c_double,
+                                                   ctypes.c_double, vp, ctypes.POINTER(ctypes.c_float)]),
+            "li_pages_workspace_size": (ctypes.c_int, [G, ctypes.POINTER(sz)]),
+            "li_pages_copy": (ctypes.c_int, [G, L_, i32, vp, vp, i32, vp, vp]),
+            "li_pages_reserve": (ctypes.c_int, [G] + [vp] * 9 + [sz, vp]),
+            "li_pages_fork": (ctypes.c_int, [G, L_, i32, vp, vp, vp, vp, vp, i32, vp, vp, vp, vp, vp, sz, vp]),
+            "li_pages_free": (ctypes.c_int, [G, vp, vp, vp, vp, i32, vp, vp, vp, vp, vp, sz, vp]),
+            "li_pages_compact": (ctypes.c_int, [G, L_, i32, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+            "li_segment_pool": (ctypes.c_int, [S_] + [vp] * 7),
+            "li_segment_select": (ctypes.c_int, [S_] + [vp] * 7),
+            "li_segment_attention": (ctypes.c_int, [S_] + [vp] * 11),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -317,3 +375,306 @@ def indexer(params: Params, query, key, weights, *, act_seq_q=None, act_seq_k=No
         li_indexer(params, query, key, weights, act_seq_q, act_seq_k, block_table, idx, vptr,
                    workspace, stream=stream)
     return idx, val
+
+
+# ---------------------------------------------------------------- rotary positions
+
+def _check_tensors(dev, **named):
+    """Device, type, size and contiguity of call arguments: name=(tensor, dtype, numel or None)."""
+    for name, (t, dtype, numel) in named.items():
+        if t.device != dev:
+            raise ValueError("%s is on %s, the call's other tensors on %s" % (name, t.device, dev))
+        if t.dtype != dtype:
+            raise TypeError("%s must be %s, not %s" % (name, dtype, t.dtype))
+        if numel is not None and (t.numel() != numel or not t.is_contiguous()):
+            raise ValueError("%s must be contiguous with %d elements, not %s" % (name, numel, tuple(t.shape)))
+
+
+def _torch_dtype(code):
+    import torch
+    return {0: torch.bfloat16, 1: torch.float16, 2: torch.float32}[code]
+
+
+def _launch(dev, f, *args, stream=None):
+    """Call a library function for tensors on `dev`: current device and stream are its."""
+    import torch
+    if dev.type != "cuda":
+        raise ValueError("the call's tensors must be on a CUDA device, not on %s" % dev)
+    if dev.index is None or dev.index == torch.cuda.current_device():
+        _check(f(*args, _stream(stream)))
+    else:
+        with torch.cuda.device(dev):
+            _check(f(*args, _stream(stream)))
+
+
+def make_rope_params(problem=None, **kw) -> RopeParams:
+    """li_rope_params from an object with its field names (dtype and pairing as
+    strings) and/or keyword overrides; mscale defaults to 1, N2 to 0 (no key)."""
+    f = {}
+    if problem is not None:
+        f.update((n, getattr(problem, n)) for n, _ in RopeParams._fields_ if hasattr(problem, n))
+    f.update(kw)
+    f.setdefault("mscale", 1.0)
+    if isinstance(f.get("dtype"), str):
+        f["dtype"] = DTYPE[f["dtype"]]
+    if isinstance(f.get("pairing"), str):
+        f["pairing"] = ROPE_PAIRING[f["pairing"]]
+    return RopeParams(**f)
+
+
+def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                     original_positions: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0):
+    """(inv_freq, mscale): radians per position of each pair (fp64 tensor on the
+    host, to be moved to the device once) and the factor for make_rope_params."""
+    import torch
+    out = torch.empty(max(1, rot_dim // 2), dtype=torch.float64)
+    m = ctypes.c_float()
+    _check(lib().li_rope_frequencies(ROPE_SCALING[scaling], rot_dim, base, factor, original_positions, beta_fast,
+                                     beta_slow, out.data_ptr(), ctypes.byref(m)))
+    return out, m.value
+
+
+def li_rope(params: RopeParams, positions, inv_freq, query, key, query_out, key_out, stream=None):
+    _check(lib().li_rope(ctypes.byref(params), _ptr(positions), _ptr(inv_freq), _ptr(query), _ptr(key),
+                         _ptr(query_out), _ptr(key_out), _stream(stream)))
+
+
+def rope(params: RopeParams, positions, inv_freq, query, key=None, *, out=None, key_out=None, stream=None):
+    """Rotate query [.., N1, D] and key [.., N2, D] by their rows' positions,
+    allocating dense outputs unless they are given (query and key themselves for
+    in place).  Returns (out, key_out or None)."""
+    import torch
+    dev, dt, p = query.device, _torch_dtype(params.dtype), params
+    _check_tensors(dev, positions=(positions, torch.int32, p.rows), inv_freq=(inv_freq, torch.float64, p.rot_dim // 2),
+                   query=(query, dt, None if p.q_row_stride or p.q_head_stride else p.rows * p.N1 * p.D))
+    if out is None:
+        out = torch.empty((p.rows, p.N1, p.D), dtype=dt, device=dev)
+    _check_tensors(dev, out=(out, dt, None if p.q_out_row_stride or p.q_out_head_stride else p.rows * p.N1 * p.D))
+    if key is not None:
+        if key_out is None:
+            key_out = torch.empty((p.rows, p.N2, p.D), dtype=dt, device=dev)
+        _check_tensors(dev, key=(key, dt, None if p.k_row_stride or p.k_head_stride else p.rows * p.N2 * p.D),
+                       key_out=(key_out, dt, None if p.k_out_row_stride or p.k_out_head_stride else p.rows * p.N2 * p.D))
+    _launch(dev, lib().li_rope, ctypes.byref(p), positions.data_ptr(), inv_freq.data_ptr(), query.data_ptr(), _ptr(key),
+            out.data_ptr(), _ptr(key_out), stream=stream)
+    return out, key_out
+
+
+# ---------------------------------------------------------------- pages of a cache
+
+def make_pages_params(**kw) -> PagesParams:
+    return PagesParams(**kw)
+
+
+def page_pools(pools):
+    """Descriptors of pool tensors [num_pages, ...] (axis 0 may be strided, a
+    page itself is contiguous), for the pages calls; they take a list too."""
+    if isinstance(pools, ctypes.Array):
+        return pools
+    arr = (PagePool * len(pools))()
+    for d, t in zip(arr, pools):
+        es = t.element_size()
+        if t.dim() < 1 or (t.shape[0] and not t[0].is_contiguous()):
+            raise ValueError("a pool's pages must be contiguous")
+        d.base = t.data_ptr()
+        d.page_bytes = (t[0].numel() if t.shape[0] else 0) * es
+        d.page_stride = max(t.stride(0) * es, d.page_bytes)
+    arr.tensors = list(pools)
+    return arr
+
+
+def li_pages_workspace_size(params: PagesParams) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().li_pages_workspace_size(ctypes.byref(params), ctypes.byref(n)))
+    return n.value
+
+
+def alloc_pages_workspace(params: PagesParams, device="cuda"):
+    import torch
+    return torch.empty(li_pages_workspace_size(params), dtype=torch.uint8, device=device)
+
+
+def _pools_on(pools, params, dev):
+    arr = page_pools(pools)
+    for t in getattr(arr, "tensors", ()):
+        if t.device != dev:
+            raise ValueError("a pool is on %s, the call's other tensors on %s" % (t.device, dev))
+        if t.shape[0] != params.num_pages:
+            raise ValueError("a pool has %d pages, not %d" % (t.shape[0], params.num_pages))
+    return arr
+
+
+def _pages_state(params, table, lens, refs, out, workspace, rows=()):
+    """Checks the state, allocates what is not given; returns (dev, out, workspace)."""
+    import torch
+    p, i32 = params, torch.int32
+    dev = table.device
+    if out is None:
+        out = (torch.empty_like(table), torch.empty_like(lens), torch.empty_like(refs))
+    if workspace is None:
+        workspace = alloc_pages_workspace(p, dev)
+    n = p.B * p.max_pages_per_seq
+    _check_tensors(dev, table=(table, i32, n), lens=(lens, i32, p.B), refs=(refs, i32, p.num_pages),
+                   table_out=(out[0], i32, n), lens_out=(out[1], i32, p.B), refs_out=(out[2], i32, p.num_pages),
+                   workspace=(workspace, torch.uint8, None))
+    for name, t, numel in rows:
+        _check_tensors(dev, **{name: (t, i32, numel)})
+    return dev, out, workspace
+
+
+def pages_copy(params: PagesParams, pools, src, dst, *, status=None, stream=None):
+    """li_pages_copy: page src[i] -> page dst[i] of every pool (int32 tensors)."""
+    import torch
+    dev, n = src.device, src.numel()
+    _check_tensors(dev, src=(src, torch.int32, n), dst=(dst, torch.int32, n))
+    arr = _pools_on(pools, params, dev)
+    _launch(dev, lib().li_pages_copy, ctypes.byref(params), arr, len(arr), src.data_ptr(), dst.data_ptr(), n,
+            _ptr(status), stream=stream)
+
+
+def pages_reserve(params: PagesParams, table, lens, refs, new_lens, *, out=None, workspace=None, status=None, stream=None):
+    """li_pages_reserve.  Returns (table, lens, refs) after the call: new
+    tensors, or `out` (which may be the inputs, for in place)."""
+    dev, out, ws = _pages_state(params, table, lens, refs, out, workspace, [("new_lens", new_lens, params.B)])
+    _launch(dev, lib().li_pages_reserve, ctypes.byref(params), table.data_ptr(), lens.data_ptr(), refs.data_ptr(),
+            new_lens.data_ptr(), out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), _ptr(status), ws.data_ptr(),
+            ws.numel(), stream=stream)
+    return out
+
+
+def pages_fork(params: PagesParams, pools, table, lens, refs, src_rows, dst_rows, *, out=None, workspace=None,
+               status=None, stream=None):
+    """li_pages_fork: row dst_rows[i] becomes a child of row src_rows[i]."""
+    n = src_rows.numel()
+    dev, out, ws = _pages_state(params, table, lens, refs, out, workspace,
+                                [("src_rows", src_rows, n), ("dst_rows", dst_rows, n)])
+    arr = _pools_on(pools, params, dev)
+    _launch(dev, lib().li_pages_fork, ctypes.byref(params), arr, len(arr), table.data_ptr(), lens.data_ptr(),
+            refs.data_ptr(), src_rows.data_ptr(), dst_rows.data_ptr(), n, out[0].data_ptr(), out[1].data_ptr(),
+            out[2].data_ptr(), _ptr(status), ws.data_ptr(), ws.numel(), stream=stream)
+    return out
+
+
+def pages_free(params: PagesParams, table, lens, refs, rows, *, out=None, workspace=None, status=None, stream=None):
+    """li_pages_free: empties the rows `rows` (int32)."""
+    n = rows.numel()
+    dev, out, ws = _pages_state(params, table, lens, refs, out, workspace, [("rows", rows, n)])
+    _launch(dev, lib().li_pages_free, ctypes.byref(params), table.data_ptr(), lens.data_ptr(), refs.data_ptr(),
+            rows.data_ptr(), n, out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), _ptr(status), ws.data_ptr(),
+            ws.numel(), stream=stream)
+    return out
+
+
+def pages_compact(params: PagesParams, pools, table, lens, refs, *, out=None, workspace=None, status=None, stream=None):
+    """li_pages_compact: the live pages become the first ones of the pool."""
+    dev, out, ws = _pages_state(params, table, lens, refs, out, workspace)
+    arr = _pools_on(pools, params, dev)
+    _launch(dev, lib().li_pages_compact, ctypes.byref(params), arr, len(arr), table.data_ptr(), lens.data_ptr(),
+            refs.data_ptr(), out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), _ptr(status), ws.data_ptr(),
+            ws.numel(), stream=stream)
+    return out
+
+
+# ---------------------------------------------------------------- segment-sparse attention
+
+def make_segment_params(problem=None, **kw) -> SegmentParams:
+    """li_segment_params from an object with its field names (layouts and dtype
+    as strings; softmax_scale 0 or absent = 1/sqrt(D)) and/or keyword overrides."""
+    f = {}
+    if problem is not None:
+        f.update((n, getattr(problem, n)) for n, _ in SegmentParams._fields_ if hasattr(problem, n))
+    f.update(kw)
+    for name in ("layout_q", "layout_kv"):
+        if isinstance(f.get(name), str):
+            f[name] = LAYOUT[f[name]]
+    if isinstance(f.get("dtype"), str):
+        f["dtype"] = DTYPE[f["dtype"]]
+    if not f.get("softmax_scale"):
+        f["softmax_scale"] = f.get("D", 128) ** -0.5
+    return SegmentParams(**f)
+
+
+def _segment_rows(p):
+    return p.B * p.S1 if p.layout_q == 0 else p.T1
+
+
+def _segment_keys(p):
+    """Elements of the key (and value) tensor, or None for a strided pool."""
+    if p.layout_kv == 2:
+        return None if p.kv_block_stride else p.num_blocks * p.block_size * p.N2 * p.D
+    return (p.B * p.S2 if p.layout_kv == 0 else p.T2) * p.N2 * p.D
+
+
+def _segment_lens(p, dev, act_seq_q, act_seq_k, block_table, status):
+    import torch
+    i32 = torch.int32
+    if act_seq_q is not None:
+        _check_tensors(dev, act_seq_q=(act_seq_q, i32, p.B))
+    if act_seq_k is not None:
+        _check_tensors(dev, act_seq_k=(act_seq_k, i32, p.B))
+    if block_table is not None and p.layout_kv == 2:
+        _check_tensors(dev, block_table=(block_table, i32, p.B * p.max_blocks_per_seq))
+    if status is not None:
+        _check_tensors(dev, status=(status, i32, 1))
+
+
+def segment_pool(params: SegmentParams, key, *, act_seq_k=None, block_table=None, first=None, pooled=None, status=None,
+                 stream=None):
+    """li_segment_pool: the segments' mean keys, fp32 [B, max_segs, N2, D].  With
+    `first` (int32 [B]) and `pooled` only the segments of the tokens from there
+    on are refreshed; segments behind a sequence keep what `pooled` holds
+    (undefined in a newly allocated one)."""
+    import torch
+    p, dev = params, key.device
+    if pooled is None:
+        if first is not None:
+            raise ValueError("first refreshes an existing pooled tensor: pass pooled")
+        pooled = torch.empty((p.B, p.max_segs, p.N2, p.D), dtype=torch.float32, device=dev)
+    _segment_lens(p, dev, None, act_seq_k, block_table, status)
+    _check_tensors(dev, key=(key, _torch_dtype(p.dtype), _segment_keys(p)),
+                   pooled=(pooled, torch.float32, p.B * p.max_segs * p.N2 * p.D))
+    if first is not None:
+        _check_tensors(dev, first=(first, torch.int32, p.B))
+    _launch(dev, lib().li_segment_pool, ctypes.byref(p), key.data_ptr(), _ptr(act_seq_k), _ptr(block_table), _ptr(first),
+            pooled.data_ptr(), _ptr(status), stream=stream)
+    return pooled
+
+
+def segment_select(params: SegmentParams, query, pooled, *, act_seq_q=None, act_seq_k=None, out=None, status=None,
+                   stream=None):
+    """li_segment_select: the chosen segments of each row and key head, int32
+    [rows, N2, seg_count], ascending, -1 behind them."""
+    import torch
+    p, dev = params, query.device
+    rows = _segment_rows(p)
+    if out is None:
+        out = torch.empty((rows, p.N2, p.seg_count), dtype=torch.int32, device=dev)
+    _segment_lens(p, dev, act_seq_q, act_seq_k, None, status)
+    _check_tensors(dev, query=(query, _torch_dtype(p.dtype), rows * p.N1 * p.D),
+                   pooled=(pooled, torch.float32, p.B * p.max_segs * p.N2 * p.D),
+                   out=(out, torch.int32, rows * p.N2 * p.seg_count))
+    _launch(dev, lib().li_segment_select, ctypes.byref(p), query.data_ptr(), pooled.data_ptr(), _ptr(act_seq_q),
+            _ptr(act_seq_k), out.data_ptr(), _ptr(status), stream=stream)
+    return out
+
+
+def segment_attention(params: SegmentParams, query, key, value, seg_idx, *, act_seq_q=None, act_seq_k=None,
+                      block_table=None, out=None, lse=None, want_lse=True, status=None, stream=None):
+    """li_segment_attention, allocating out [rows, N1, D] (the query's dtype) and,
+    when asked, lse [rows, N1] fp32.  Returns (out, lse or None)."""
+    import torch
+    p, dev, dt = params, query.device, _torch_dtype(params.dtype)
+    rows, keys = _segment_rows(p), _segment_keys(p)
+    if out is None:
+        out = torch.empty((rows, p.N1, p.D), dtype=dt, device=dev)
+    if lse is None and want_lse:
+        lse = torch.empty((rows, p.N1), dtype=torch.float32, device=dev)
+    _segment_lens(p, dev, act_seq_q, act_seq_k, block_table, status)
+    _check_tensors(dev, query=(query, dt, rows * p.N1 * p.D), key=(key, dt, keys), value=(value, dt, keys),
+                   seg_idx=(seg_idx, torch.int32, rows * p.N2 * p.seg_count), out=(out, dt, rows * p.N1 * p.D))
+    if lse is not None:
+        _check_tensors(dev, lse=(lse, torch.float32, rows * p.N1))
+    _launch(dev, lib().li_segment_attention, ctypes.byref(p), query.data_ptr(), key.data_ptr(), value.data_ptr(),
+            seg_idx.data_ptr(), _ptr(act_seq_q), _ptr(act_seq_k), _ptr(block_table), out.data_ptr(), _ptr(lse),
+            _ptr(status), stream=stream)
+    return out, lse
