@@ -591,3 +591,11 @@ void li_set_profile_events(void *const *events, int32_t n)
 int32_t li_last_launch_count(void) { return g_launches; }
 
 }  // extern "C"
+
+namespace li {
+li_status tensor_map_16bit(CUtensorMap *m, const void *base, int rank, const uint64_t *dims,
+                           const uint64_t *strides_bytes, const uint32_t *box, const char *what)
+{
+    return encode(m, 2, base, rank, dims, strides_bytes, box, what);
+}
+}  // namespace li

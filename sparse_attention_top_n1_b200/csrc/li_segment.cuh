@@ -2,6 +2,7 @@
 // attention): which batch and position a query row has, how many keys it sees,
 // and where a key lies.
 #pragma once
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -114,4 +115,7 @@ li_status seg_setup(const char *call, const li_segment_params *p, bool queries, 
                     const int32_t *act_k, const int32_t *block_table, int32_t *status, SegGeo *g);
 li_status seg_fail(const char *call, li_status st, const char *what);
 int seg_sms();
+// A tensor map over 16-bit elements with the 128-byte swizzle; zeros outside.
+li_status tensor_map_16bit(CUtensorMap *m, const void *base, int rank, const uint64_t *dims, const uint64_t *strides_bytes,
+                           const uint32_t *box, const char *what);
 }  // namespace li
