@@ -16,15 +16,16 @@
 // tiles of 64 keys made of quanta (64, 32 or 16 keys that lie in one segment
 // and one page).  A cluster of C CTAs takes the tiles in turn when blocks are
 // few and merges its partial results through distributed shared memory.
-//   warps 0-3  softmax, a thread per tensor-core row: scores out of tensor
-//              memory, -inf where the row does not take the key, weights
-//              exp2(s - m) rounded to the input type back into tensor memory
-//              over the scores they came from; m moves only when a tile beats it
-//              by 2^8, and only then O is rescaled; the sum is of the weights
+//   warps 0-7  softmax, two threads per tensor-core row (half of the tile's keys
+//              each): scores out of tensor memory, -inf where the row does not
+//              take the key, weights exp2(s - m) rounded to the input type back
+//              into tensor memory over the scores they came from; m moves only
+//              when a tile beats it by 2^8, and only then the two threads
+//              exchange their maxima and O is rescaled; the sum is of the weights
 //              before rounding, so lse is an fp32 result
-//   warp 4     TMA: a key and a value box per quantum; empty slots take
+//   warp 8     TMA: a key and a value box per quantum; empty slots take
 //              coordinates outside the tensor, which read as zeros
-//   warp 5     S = Q K^T (Q from tensor memory), O += P V (P from tensor memory)
+//   warp 9     S = Q K^T (Q from tensor memory), O += P V (P from tensor memory)
 // A key that a row does not take has weight 0 in it, but 0 * inf is NaN: values
 // behind the last key that the block sees are zeroed in shared memory, and a
 // result that is not finite although its sum of weights is, is computed again by
@@ -48,7 +49,8 @@ using namespace li;
 
 constexpr int kM = 128;                   // tensor-core rows
 constexpr int kTile = 64;                 // keys of a tile
-constexpr int kThreads = 192;
+constexpr int kSoftWarps = 8;
+constexpr int kThreads = 32 * (kSoftWarps + 2);
 constexpr int kWarps = kThreads / 32;
 constexpr int kPlane = kTile * 128;       // bytes of 64 columns of a tile
 constexpr int kMember = 1024;             // membership words, and most listed segments, of a round
@@ -85,10 +87,11 @@ struct Layout {
     static constexpr int CURSOR = VIS + kM * 4;             // int32 [kM]
     static constexpr int LAST = CURSOR + kM * 4;            // int32 [kM]
     static constexpr int MERGE = LAST + kM * 4;             // float [3][kM]
-    static constexpr int META = MERGE + 3 * kM * 4;         // int2 [kMetaRing][4]
+    static constexpr int TOP = MERGE + 3 * kM * 4;          // float [2][kM]: maxima, then sums, of the half rows
+    static constexpr int META = TOP + 2 * kM * 4;         // int2 [kMetaRing][4]
     static constexpr int BALL = META + kMetaRing * 32;      // uint32 [32]
     static constexpr int BARS = BALL + 32 * 4;
-    static constexpr int NBARS = 4 * STAGES + 2 + 2 + 1 + 1 + kMetaRing;
+    static constexpr int NBARS = 4 * STAGES + 2 + 2 + 1 + 1 + 1 + kMetaRing;
     static constexpr int MISC = BARS + NBARS * 8;           // int32 [16]
     static constexpr int END = MISC + 64;
     static constexpr int BYTES = END + 1024;
@@ -126,6 +129,34 @@ __device__ __forceinline__ int32_t scan_add(int32_t v, int lane)
         if (lane >= o) v += u;
     }
     return v;
+}
+
+// Whether `p` holds in any thread of a pair of warps (64 threads on barrier `id`).
+__device__ __forceinline__ bool pair_any(int id, bool p)
+{
+    uint32_t any;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, %2, 64, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(any)
+        : "r"((uint32_t)p), "r"(id)
+        : "memory");
+    return any != 0;
+}
+__device__ __forceinline__ void pair_sync(int id) { asm volatile("barrier.cta.sync %0, 64;" ::"r"(id) : "memory"); }
+
+// One lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t one;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(one));
+    return one != 0;
 }
 
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) < INFINITY; }
@@ -203,11 +234,13 @@ segattn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_k, cons
     int32_t *svis = reinterpret_cast<int32_t *>(base + L::VIS);
     int32_t *cursor = reinterpret_cast<int32_t *>(base + L::CURSOR);
     int32_t *lastof = reinterpret_cast<int32_t *>(base + L::LAST);
+    float *tops = reinterpret_cast<float *>(base + L::TOP);
     int2 *meta = reinterpret_cast<int2 *>(base + L::META);
     uint32_t *ball = reinterpret_cast<uint32_t *>(base + L::BALL);
     uint64_t *kfull = reinterpret_cast<uint64_t *>(base + L::BARS), *kempty = kfull + NS;
     uint64_t *vfull = kempty + NS, *vempty = vfull + NS;
-    uint64_t *sfull = vempty + NS, *pfull = sfull + 2, *qfull = pfull + 2, *pvdone = qfull + 1, *mfull = pvdone + 1;
+    uint64_t *sfull = vempty + NS, *pfull = sfull + 2, *qfull = pfull + 2, *pvdone = qfull + 1, *odone = pvdone + 1,
+             *mfull = odone + 1;
     int32_t *misc = reinterpret_cast<int32_t *>(base + L::MISC);
     uint32_t *tslot = reinterpret_cast<uint32_t *>(misc);
     volatile int *abort_flag = misc + 1;
@@ -216,7 +249,7 @@ segattn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_k, cons
     uint32_t *bad = reinterpret_cast<uint32_t *>(misc + 9);   // [4] results to compute again
 
     const SegGeo &g = a.g;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int32_t blk = blockIdx.x / C, n = blockIdx.y;
     const int rank = C > 1 ? (int)(blockIdx.x % C) : 0;
 
@@ -267,12 +300,13 @@ segattn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_k, cons
         }
         mbar_init(&sfull[0], 1);
         mbar_init(&sfull[1], 1);
-        // the four softmax warps; one barrier per score buffer, since a warp without
+        // the softmax warps; one barrier per score buffer, since a warp without
         // rows may be a tile ahead of the others
-        mbar_init(&pfull[0], 4);
-        mbar_init(&pfull[1], 4);
-        mbar_init(qfull, 4);
+        mbar_init(&pfull[0], kSoftWarps);
+        mbar_init(&pfull[1], kSoftWarps);
+        mbar_init(qfull, kSoftWarps);
         mbar_init(pvdone, 1);
+        mbar_init(odone, 1);
         for (int s = 0; s < kMetaRing; ++s) mbar_init(&mfull[s], 1);
         *abort_flag = 0;
         bad[0] = bad[1] = bad[2] = bad[3] = 0;
@@ -281,7 +315,7 @@ segattn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_k, cons
     __syncthreads();
     const int32_t b = where[0], row0 = where[1], nr = where[2], i0 = where[3], Sq = where[4];
     if (nr <= 0) return;                                 // the whole cluster
-    if (warp == 5) tmem_alloc(tslot, 256);
+    if (warp == kSoftWarps + 1) tmem_alloc(tslot, 256);
     int64_t k_off;
     const int32_t Sk = seg_keys(g, b, k_off);
     const int32_t segs = (int32_t)(((int64_t)Sk + g.seg - 1) / g.seg);
@@ -297,8 +331,11 @@ segattn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_k, cons
         lastof[tid] = -1;
     }
     const int32_t lanes = nr * g.G;                      // tensor-core rows in use
-    const int32_t rl = tid / g.G;                        // softmax threads: the query row
-    const bool used = tid < lanes;
+    const int32_t x = tid % kM, side = tid / kM;         // softmax threads: the tensor-core row, half of its columns
+    const int32_t rl = x / g.G;                          // its query row
+    const bool used = x < lanes;
+    const uint32_t tlane = (uint32_t)((warp & 3) * 32) << 16;
+    const int64_t at = (int64_t)(row0 + rl) * g.N1 + n * g.G + (x - rl * g.G);
     const bool listed_alone = nr == 1;
     const int32_t MW = (nr + 31) >> 5, W = (kMember / MW) & ~31;
 
@@ -318,7 +355,7 @@ segattn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_k, cons
         __syncthreads();
         if (first) {
             tc_fence_after_sync();
-            tmem = *tslot;
+            tmem = __shfl_sync(0xffffffffu, *tslot, 0);
         }
         auto entries = [&](int32_t r) { return a.idx + ((int64_t)(row0 + r) * g.N2 + n) * g.count; };
         int32_t listed = 0;
@@ -408,24 +445,24 @@ segattn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_k, cons
         const int32_t tiles = (nq + slots - 1) / slots;
         const int32_t mine = tiles > rank ? (tiles - rank + C - 1) / C : 0;
 
-        if (warp < 4) {
+        if (warp < kSoftWarps) {
             // ------------------------------------------------------------ softmax
-            const uint32_t tlane = (uint32_t)(warp * 32) << 16;
             if (first) {
-                // the row's query into tensor memory (lanes without a row: zeros)
+                // the queries into tensor memory, half a row per thread (rows without one: zeros)
+                uint4 qv[D / 16] = {};
+                if (used) {
+                    const uint4 *src = reinterpret_cast<const uint4 *>(a.q + at * D + side * (D / 2));
 #pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
-                    uint32_t w[16] = {};
-                    if (used) {
-                        const uint4 *src = reinterpret_cast<const uint4 *>(
-                            a.q + ((int64_t)(row0 + rl) * g.N1 + n * g.G + (tid - rl * g.G)) * D + 32 * c);
+                    for (int e = 0; e < D / 16; ++e) qv[e] = src[e];
+                }
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const uint4 x = src[e];
-                            w[4 * e] = x.x, w[4 * e + 1] = x.y, w[4 * e + 2] = x.z, w[4 * e + 3] = x.w;
-                        }
-                    }
-                    tmem_st16(tmem + kColQ + 16 * c + tlane, w);
+                for (int c = 0; c < D / 64; ++c) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        w[4 * e] = qv[4 * c + e].x, w[4 * e + 1] = qv[4 * c + e].y, w[4 * e + 2] = qv[4 * c + e].z,
+                              w[4 * e + 3] = qv[4 * c + e].w;
+                    tmem_st16(tmem + kColQ + side * (D / 4) + 16 * c + tlane, w);
                 }
                 tmem_st_wait();
                 tc_fence_before_sync();
@@ -452,68 +489,71 @@ segattn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_k, cons
                 }
                 wait_phase(&sfull[sb], (SB == 2 ? u >> 1 : u) & 1, g.status, abort_flag);
                 tc_fence_after_sync();
-                if (__any_sync(0xffffffffu, mask != 0)) {
-                    uint32_t sq[4][16];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_ld16(ts + 16 * c, sq[c]);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_ld_wait16(sq[c]);
+                if (__any_sync(0xffffffffu, mask != 0)) {        // the same for both warps of a pair
+                    uint32_t sq[2][16];
+                    tmem_ld16(ts + side * 32, sq[0]);
+                    tmem_ld16(ts + side * 32 + 16, sq[1]);
+                    tmem_ld_wait16(sq[0]);
+                    tmem_ld_wait16(sq[1]);
                     auto sv = [&](int j) -> uint32_t & { return sq[j >> 4][j & 15]; };
-                    if (!__all_sync(0xffffffffu, mask == ~0ull)) {
-                        const uint32_t k0 = (uint32_t)mask, k1 = (uint32_t)(mask >> 32);
+                    const uint32_t mine_of = (uint32_t)(mask >> (32 * side));
+                    if (!__all_sync(0xffffffffu, mine_of == 0xffffffffu)) {
 #pragma unroll
-                        for (int j = 0; j < 64; ++j)
-                            if (!(((j < 32 ? k0 : k1) >> (j & 31)) & 1u)) sv(j) = 0xff800000u;
+                        for (int j = 0; j < 32; ++j)
+                            if (!(mine_of >> j & 1u)) sv(j) = 0xff800000u;
                     }
-                    float mx[22];
+                    float mx[11];
 #pragma unroll
-                    for (int j = 0; j < 21; ++j)
+                    for (int j = 0; j < 10; ++j)
                         mx[j] = fmax3(__uint_as_float(sv(3 * j)), __uint_as_float(sv(3 * j + 1)),
                                       __uint_as_float(sv(3 * j + 2)));
-                    mx[21] = __uint_as_float(sv(63));
-#pragma unroll
-                    for (int j = 0; j < 7; ++j) mx[j] = fmax3(mx[3 * j], mx[3 * j + 1], mx[3 * j + 2]);
-                    const float mt = fmaxf(fmaxf(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5])),
-                                           fmaxf(mx[6], mx[21])) * a.scale_log2;
+                    mx[10] = fmaxf(__uint_as_float(sv(30)), __uint_as_float(sv(31)));
+                    float mt = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]),
+                                     fmax3(fmax3(mx[6], mx[7], mx[8]), mx[9], mx[10])) * a.scale_log2;
+                    // (the barrier also stands between the pair's reads of the scores and its
+                    // writes of the weights over them)
                     float alpha = 1.f;
-                    if (mt > m_run + kRescaleLog2 || (m_run == -INFINITY && mt > -INFINITY)) {
-                        alpha = m_run == -INFINITY ? 0.f : ex2(m_run - mt);
-                        m_run = mt;
+                    if (pair_any(1 + (warp & 3), mt > m_run + kRescaleLog2 || (m_run == -INFINITY && mt > -INFINITY))) {
+                        tops[side * kM + x] = mt;
+                        pair_sync(1 + (warp & 3));
+                        mt = fmaxf(mt, tops[(side ^ 1) * kM + x]);
+                        if (mt > m_run + kRescaleLog2 || (m_run == -INFINITY && mt > -INFINITY)) {
+                            alpha = m_run == -INFINITY ? 0.f : ex2(m_run - mt);
+                            m_run = mt;
+                        }
                     }
                     const float mb = m_run == -INFINITY ? 0.f : -m_run;
-                    float rs[4][2] = {};
-                    uint32_t pk[2][16];
+                    float rs[2][2] = {};
+                    uint32_t pk[16];
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
+                    for (int j = 0; j < 16; ++j) {
                         float x0, x1;
                         ffma2(x0, x1, __uint_as_float(sv(2 * j)), __uint_as_float(sv(2 * j + 1)), a.scale_log2,
                               a.scale_log2, mb, mb);
                         x0 = ex2(x0);
                         x1 = ex2(x1);
-                        pk[j >> 4][j & 15] = pack2<F16>(x0, x1);
-                        fadd2(rs[j & 3][0], rs[j & 3][1], x0, x1);
+                        pk[j] = pack2<F16>(x0, x1);
+                        fadd2(rs[j & 1][0], rs[j & 1][1], x0, x1);
                     }
-                    l_run = l_run * alpha + ((rs[0][0] + rs[2][0]) + (rs[1][0] + rs[3][0])) +
-                            ((rs[0][1] + rs[2][1]) + (rs[1][1] + rs[3][1]));
-                    tmem_st16(ts, pk[0]);
-                    tmem_st16(ts + 16, pk[1]);
+                    l_run = l_run * alpha + ((rs[0][0] + rs[1][0]) + (rs[0][1] + rs[1][1]));
+                    tmem_st16(ts + side * 16, pk);
                     if (u > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
                         wait_phase(pvdone, (u - 1) & 1, g.status, abort_flag);
                         tc_fence_after_sync();
 #pragma unroll
-                        for (int c = 0; c < D / 16; ++c) {
+                        for (int c = 0; c < D / 32; ++c) {
                             uint32_t o[16];
-                            tmem_ld16(tmem + tlane + 16 * c, o);
+                            const uint32_t to = tmem + tlane + side * (D / 2) + 16 * c;
+                            tmem_ld16(to, o);
                             tmem_ld_wait16(o);
 #pragma unroll
                             for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                            tmem_st16(tmem + tlane + 16 * c, o);
+                            tmem_st16(to, o);
                         }
                     }
                 } else {
                     const uint32_t none[16] = {};
-                    tmem_st16(ts, none);
-                    tmem_st16(ts + 16, none);
+                    tmem_st16(ts + side * 16, none);
                 }
                 tmem_st_wait();
                 if (cut >= 0) {
@@ -521,7 +561,7 @@ segattn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_k, cons
                     const uint32_t vs = u % NS;
                     wait_phase(&vfull[vs], (u / NS) & 1, g.status, abort_flag);
                     const int r0 = cut * Q + cut_at, rows = (cut + 1) * Q - r0;
-                    for (int e = tid; e < rows * (D / 8); e += kM) {
+                    for (int e = tid; e < rows * (D / 8); e += 32 * kSoftWarps) {
                         const int r = r0 + e / (D / 8), ch = e % (D / 8);
                         *reinterpret_cast<uint4 *>(base + L::V + vs * L::STAGE + (ch >> 3) * kPlane + r * 128 +
                                                    (ch & 7) * 16) = make_uint4(0, 0, 0, 0);
@@ -532,7 +572,7 @@ segattn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_k, cons
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&pfull[sb]);
             }
-        } else if (warp == 4) {
+        } else if (warp == kSoftWarps) {
             // ------------------------------------------------------------ copies
             const bool paged = g.layout_kv == LI_PA_BSND;
             const int32_t batch = 32 / slots;            // tiles whose slots the warp's lanes hold
@@ -591,42 +631,57 @@ segattn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_k, cons
                                     n * D + 64 * p, c1, c2);
                 }
             }
-        } else if (lane == 0) {
+        } else {
             // ------------------------------------------------------------ products
+            // (the whole warp runs the loop and one lane issues: addresses and
+            // descriptors then stay in uniform registers)
+            const bool leader = elect_one();
             const uint32_t fmt = F16 ? 0u : 1u, sbase = smem_u32(base);
             const uint32_t id_s = make_idesc(fmt, fmt, kM, kTile);
             const uint32_t id_pv = make_idesc(fmt, fmt, kM, D) | (1u << 16);      // values MN-major
+            const int32_t todo = __shfl_sync(0xffffffffu, mine, 0);
             if (first) wait_phase(qfull, 0, g.status, abort_flag);   // the queries stand in tensor memory
-            auto weigh = [&](uint32_t x) {               // O += P V of tile x
-                const uint32_t st = x % NS, sb = SB == 2 ? x & 1 : 0;
-                wait_phase(&pfull[sb], (SB == 2 ? x >> 1 : x) & 1, g.status, abort_flag);
-                wait_phase(&vfull[st], (x / NS) & 1, g.status, abort_flag);
+            auto weigh = [&](uint32_t t) {               // O += P V of tile t
+                const uint32_t st = t % NS, sb = SB == 2 ? t & 1 : 0;
+                wait_phase(&pfull[sb], (SB == 2 ? t >> 1 : t) & 1, g.status, abort_flag);
+                wait_phase(&vfull[st], (t / NS) & 1, g.status, abort_flag);
                 tc_fence_after_sync();
-                const uint32_t vb = sbase + L::V + st * L::STAGE;
+                __syncwarp();
+                if (leader) {
+                    const uint64_t vd = smem_desc_sw128_mn(sbase + L::V + st * L::STAGE, kPlane, 1024);
 #pragma unroll
-                for (int kk = 0; kk < kTile / 16; ++kk)
-                    mma_f16_ta(tmem, tmem + kColS + sb * kTile + 8 * kk,
-                               smem_desc_sw128_mn(vb + kk * 16 * 128, kPlane, 1024), id_pv, (x > 0 || kk > 0) ? 1u : 0u);
-                mma_commit(&vempty[st]);
-                mma_commit(pvdone);
+                    for (int kk = 0; kk < kTile / 16; ++kk)
+                        mma_f16_ta(tmem, tmem + kColS + sb * kTile + 8 * kk, vd + kk * (16 * 128 / 16), id_pv,
+                                   (t > 0 || kk > 0) ? 1u : 0u);
+                    mma_commit(&vempty[st]);
+                    mma_commit(pvdone);
+                }
+                __syncwarp();
             };
-            for (int32_t k = 0; k < mine; ++k, ++u) {
+            for (int32_t k = 0; k < todo; ++k, ++u) {
                 const uint32_t st = u % NS, sb = SB == 2 ? u & 1 : 0;
                 wait_phase(&kfull[st], (u / NS) & 1, g.status, abort_flag);
                 // the buffer's last weights have been read
                 if (u >= SB) wait_phase(pvdone, (u - SB) & 1, g.status, abort_flag);
                 tc_fence_after_sync();
-                const uint32_t kb = sbase + L::K + st * L::STAGE;
+                __syncwarp();
+                if (leader) {
+                    const uint64_t kd = smem_desc_sw128(sbase + L::K + st * L::STAGE);
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-                    mma_f16_ta(tmem + kColS + sb * kTile, tmem + kColQ + 8 * kk,
-                               smem_desc_sw128(kb + (kk >> 2) * kPlane + (kk & 3) * 32), id_s, kk != 0);
-                mma_commit(&sfull[sb]);
-                mma_commit(&kempty[st]);
+                    for (int kk = 0; kk < D / 16; ++kk)
+                        mma_f16_ta(tmem + kColS + sb * kTile, tmem + kColQ + 8 * kk,
+                                   kd + ((kk >> 2) * kPlane + (kk & 3) * 32) / 16, id_s, kk != 0);
+                    mma_commit(&sfull[sb]);
+                    mma_commit(&kempty[st]);
+                }
+                __syncwarp();
                 if (SB == 1) weigh(u);
                 else if (k > 0) weigh(u - 1);
             }
-            if (SB == 2 && mine > 0) weigh(u - 1);
+            if (SB == 2 && todo > 0) weigh(u - 1);
+            // a barrier of its own for the end: whoever waits for it late must not
+            // take a later phase of pvdone for an earlier one
+            if (next == kNone && leader) mma_commit(odone);
         }
         __syncwarp();
         if (next == kNone) break;                        // the same for every thread, and every CTA of the cluster
@@ -636,58 +691,53 @@ segattn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_k, cons
 
     // -------------------------------------------------------------------- results
     // every role has counted this CTA's tiles in u
-    if (warp < 4) {
-        const uint32_t tlane = (uint32_t)(warp * 32) << 16;
+    if (warp < kSoftWarps) {
         if (u > 0) {
-            if (SB == 2 && u > 1) wait_phase(pvdone, (u - 2) & 1, g.status, abort_flag);   // in order: a parity names two phases
-            wait_phase(pvdone, (u - 1) & 1, g.status, abort_flag);
+            wait_phase(odone, 0, g.status, abort_flag);
             tc_fence_after_sync();
         }
-        const int64_t at = (int64_t)(row0 + rl) * g.N1 + n * g.G + (tid - rl * g.G);
+        tops[side * kM + x] = l_run;
+        pair_sync(1 + (warp & 3));
+        l_run += tops[(side ^ 1) * kM + x];              // (of two summands: the same in both threads)
         float *sO = reinterpret_cast<float *>(base);     // [kM][D], 16-byte chunks of row r at c ^ (r & 15)
         const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
         bool odd = false;
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
-            uint32_t o[16];
+        for (int c = 0; c < D / 32; ++c) {
+            const int col = side * (D / 2) + 16 * c;
+            uint32_t o[16] = {};
             if (u > 0) {
-                tmem_ld16(tmem + tlane + 16 * c, o);
+                tmem_ld16(tmem + tlane + col, o);
                 tmem_ld_wait16(o);
             }
             if constexpr (C == 1) {
                 uint32_t w[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const float x = u > 0 ? __uint_as_float(o[2 * e]) * inv : 0.f;
-                    const float y = u > 0 ? __uint_as_float(o[2 * e + 1]) * inv : 0.f;
-                    odd |= !finite(x) || !finite(y);
-                    w[e] = pack2<F16>(x, y);
+                    const float y0 = __uint_as_float(o[2 * e]) * inv, y1 = __uint_as_float(o[2 * e + 1]) * inv;
+                    odd |= !finite(y0) || !finite(y1);
+                    w[e] = pack2<F16>(y0, y1);
                 }
                 if (used) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(a.out + at * D + 16 * c);
+                    uint4 *dst = reinterpret_cast<uint4 *>(a.out + at * D + col);
                     dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
                     dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
                 }
             } else {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int ch = 4 * c + e;
-                    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (u > 0)
-                        x = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
-                                        __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
-                    reinterpret_cast<float4 *>(sO)[tid * (D / 4) + (ch ^ (tid & 15))] = x;
-                }
+                for (int e = 0; e < 4; ++e)
+                    reinterpret_cast<uint4 *>(sO)[x * (D / 4) + ((col / 4 + e) ^ (x & 15))] =
+                        make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
             }
         }
         if constexpr (C == 1) {
             const uint32_t m = __ballot_sync(0xffffffffu, used && odd && finite(l_run));
-            if (lane == 0) bad[warp] = m;
-            if (used && a.lse) a.lse[at] = l_run == 0.f ? -INFINITY : (m_run + log2f(l_run)) * kLn2;
-        } else {
+            if (lane == 0 && m) atomicOr(&bad[warp & 3], m);
+            if (side == 0 && used && a.lse) a.lse[at] = l_run == 0.f ? -INFINITY : (m_run + log2f(l_run)) * kLn2;
+        } else if (side == 0) {
             float *sM = reinterpret_cast<float *>(base + L::MERGE);
-            sM[tid] = m_run;
-            sM[kM + tid] = l_run;
+            sM[x] = m_run;
+            sM[kM + x] = l_run;
         }
     }
     if constexpr (C > 1) {
@@ -698,25 +748,25 @@ segattn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_k, cons
         cl.sync();
         const int32_t share = (lanes + C - 1) / C, from = rank * share;
         const int32_t cnt = lanes - from < share ? (lanes > from ? lanes - from : 0) : share;
-        auto out_at = [&](int32_t x) { return (int64_t)(row0 + x / g.G) * g.N1 + n * g.G + x % g.G; };
+        auto out_at = [&](int32_t y) { return (int64_t)(row0 + y / g.G) * g.N1 + n * g.G + y % g.G; };
         float *sums = sWt;                               // weight of partial r for row x: [share][C]
         for (int e = tid; e < cnt * C; e += kThreads) {
-            const int x = from + e / C, r = e % C;
+            const int y = from + e / C, r = e % C;
             float top = -INFINITY, sum = 0.f;
 #pragma unroll
-            for (int p = 0; p < C; ++p) top = fmaxf(top, cl.map_shared_rank(sM, p)[x]);
+            for (int p = 0; p < C; ++p) top = fmaxf(top, cl.map_shared_rank(sM, p)[y]);
 #pragma unroll
             for (int p = 0; p < C; ++p) {
-                const float mp = cl.map_shared_rank(sM, p)[x], lp = cl.map_shared_rank(sL, p)[x];
+                const float mp = cl.map_shared_rank(sM, p)[y], lp = cl.map_shared_rank(sL, p)[y];
                 if (lp != 0.f) sum += lp * (mp == -INFINITY ? 1.f : exp2f(mp - top));
             }
-            const float mr = cl.map_shared_rank(sM, r)[x], lr = cl.map_shared_rank(sL, r)[x];
+            const float mr = cl.map_shared_rank(sM, r)[y], lr = cl.map_shared_rank(sL, r)[y];
             sums[e] = lr == 0.f ? 0.f : (mr == -INFINITY ? 1.f : exp2f(mr - top)) / sum;
-            if (r == 0 && a.lse) a.lse[out_at(x)] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+            if (r == 0 && a.lse) a.lse[out_at(y)] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
         }
         __syncthreads();
         for (int e = tid; e < cnt * (D / 4); e += kThreads) {
-            const int hl = e / (D / 4), ch = e % (D / 4), x = from + hl;
+            const int hl = e / (D / 4), ch = e % (D / 4), y = from + hl;
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
             bool whole = true;                           // every weight is finite
 #pragma unroll
@@ -724,7 +774,7 @@ segattn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_k, cons
                 const float w = sums[hl * C + r];
                 whole &= finite(w);
                 if (w != 0.f) {
-                    const float4 o = reinterpret_cast<const float4 *>(cl.map_shared_rank(sO, r))[x * (D / 4) + (ch ^ (x & 15))];
+                    const float4 o = reinterpret_cast<const float4 *>(cl.map_shared_rank(sO, r))[y * (D / 4) + (ch ^ (y & 15))];
                     acc.x = fmaf(w, o.x, acc.x);
                     acc.y = fmaf(w, o.y, acc.y);
                     acc.z = fmaf(w, o.z, acc.z);
@@ -732,8 +782,8 @@ segattn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_k, cons
                 }
             }
             if (whole && !(finite(acc.x) && finite(acc.y) && finite(acc.z) && finite(acc.w)))
-                atomicOr(&bad[x >> 5], 1u << (x & 31));
-            *reinterpret_cast<uint2 *>(a.out + out_at(x) * D + 4 * ch) =
+                atomicOr(&bad[y >> 5], 1u << (y & 31));
+            *reinterpret_cast<uint2 *>(a.out + out_at(y) * D + 4 * ch) =
                 make_uint2(pack2<F16>(acc.x, acc.y), pack2<F16>(acc.z, acc.w));
         }
         cl.sync();                                       // every peer has read this CTA's partials
@@ -741,11 +791,11 @@ segattn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_k, cons
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    if (warp == 5) tmem_dealloc(tmem, 256);
+    if (warp == kSoftWarps + 1) tmem_dealloc(tmem, 256);
     for (int w = 0; w < 4; ++w)
         for (uint32_t m = bad[w]; m; m &= m - 1) {
-            const int32_t x = 32 * w + __ffs(m) - 1;
-            attend_plainly<D, F16>(a, base, row0 + x / g.G, n * g.G + x % g.G);
+            const int32_t y = 32 * w + __ffs(m) - 1;
+            attend_plainly<D, F16>(a, base, row0 + y / g.G, n * g.G + y % g.G);
         }
 }
 
