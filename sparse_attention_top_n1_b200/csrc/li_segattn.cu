@@ -25,7 +25,7 @@
 //              before rounding, so lse is an fp32 result
 //   warp 8     TMA: a key and a value box per quantum; empty slots take
 //              coordinates outside the tensor, which read as zeros
-//   warp 9     S = Q K^T (Q from tensor memory), O += P V (P from tensor memory)
+//   warp 9     S = Q K^T one tile ahead of O += P V (P from tensor memory)
 // A key that a row does not take has weight 0 in it, but 0 * inf is NaN: values
 // behind the last key that the block sees are zeroed in shared memory, and a
 // result that is not finite although its sum of weights is, is computed again by
@@ -54,7 +54,6 @@ constexpr int kThreads = 32 * (kSoftWarps + 2);
 constexpr int kWarps = kThreads / 32;
 constexpr int kPlane = kTile * 128;       // bytes of 64 columns of a tile
 constexpr int kMember = 1024;             // membership words, and most listed segments, of a round
-constexpr int kMetaRing = 8;              // tiles whose slots are described at a time
 constexpr int kMaxSplit = 8;
 constexpr float kRescaleLog2 = 8.f;
 constexpr float kLn2 = 0.69314718055994531f;
@@ -77,21 +76,25 @@ struct AttnArgs {
 // 128-byte rows in 64-column planes with the 128-byte swizzle.
 template <int D>
 struct Layout {
-    static constexpr int STAGES = D == 128 ? 3 : 4;
+    static constexpr bool QT = D == 64;                     // queries in tensor memory; beside a 128-column O there is room
+                                                            // for two score buffers only with the queries in shared memory
+    static constexpr int STAGES = D == 128 ? 2 : 4;
     static constexpr int STAGE = kTile * D * 2;
-    static constexpr int K = 0;
+    static constexpr int Q = 0;                             // [D/64][kM][128 B]
+    static constexpr int K = QT ? 0 : kM * D * 2;
     static constexpr int V = K + STAGES * STAGE;
     static constexpr int MEMBER = V + STAGES * STAGE;       // uint32 [kMember]
     static constexpr int LIST = MEMBER + kMember * 4;       // int32 [kMember]
     static constexpr int VIS = LIST + kMember * 4;          // int32 [kM]
     static constexpr int CURSOR = VIS + kM * 4;             // int32 [kM]
     static constexpr int LAST = CURSOR + kM * 4;            // int32 [kM]
-    static constexpr int MERGE = LAST + kM * 4;             // float [3][kM]
-    static constexpr int TOP = MERGE + 3 * kM * 4;          // float [2][kM]: maxima, then sums, of the half rows
-    static constexpr int META = TOP + 2 * kM * 4;         // int2 [kMetaRing][4]
-    static constexpr int BALL = META + kMetaRing * 32;      // uint32 [32]
+    static constexpr int MERGE = MEMBER;                    // float [3][kM], when the tiles are done
+    static constexpr int TOP = LAST + kM * 4;               // float [2][kM]: maxima, then sums, of the half rows
+    static constexpr int RING = STAGES + 2;                 // tiles whose masks are held at a time
+    static constexpr int MASK = TOP + 2 * kM * 4;           // uint64 [RING][kM]: the keys that a query row takes
+    static constexpr int BALL = MASK + RING * kM * 8;       // uint32 [32]
     static constexpr int BARS = BALL + 32 * 4;
-    static constexpr int NBARS = 4 * STAGES + 2 + 2 + 1 + 1 + 1 + kMetaRing;
+    static constexpr int NBARS = 4 * STAGES + 2 + 2 + 1 + 1 + 1 + RING;
     static constexpr int MISC = BARS + NBARS * 8;           // int32 [16]
     static constexpr int END = MISC + 64;
     static constexpr int BYTES = END + 1024;
@@ -225,8 +228,7 @@ segattn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_k, cons
 {
     using L = Layout<D>;
     constexpr int NS = L::STAGES;
-    constexpr int SB = D == 64 ? 2 : 1;                  // score buffers: 256 columns hold two only beside a 64-column O
-    constexpr int kColQ = D, kColS = D == 64 ? 128 : 192;
+    constexpr int kColQ = D, kColS = 128;                // tensor memory: O at 0, then the queries (D = 64), two score buffers
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint32_t *member = reinterpret_cast<uint32_t *>(base + L::MEMBER);
@@ -235,7 +237,7 @@ segattn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_k, cons
     int32_t *cursor = reinterpret_cast<int32_t *>(base + L::CURSOR);
     int32_t *lastof = reinterpret_cast<int32_t *>(base + L::LAST);
     float *tops = reinterpret_cast<float *>(base + L::TOP);
-    int2 *meta = reinterpret_cast<int2 *>(base + L::META);
+    uint64_t *masks = reinterpret_cast<uint64_t *>(base + L::MASK);
     uint32_t *ball = reinterpret_cast<uint32_t *>(base + L::BALL);
     uint64_t *kfull = reinterpret_cast<uint64_t *>(base + L::BARS), *kempty = kfull + NS;
     uint64_t *vfull = kempty + NS, *vempty = vfull + NS;
@@ -307,7 +309,7 @@ segattn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_k, cons
         mbar_init(qfull, kSoftWarps);
         mbar_init(pvdone, 1);
         mbar_init(odone, 1);
-        for (int s = 0; s < kMetaRing; ++s) mbar_init(&mfull[s], 1);
+        for (int s = 0; s < L::RING; ++s) mbar_init(&mfull[s], 1);
         *abort_flag = 0;
         bad[0] = bad[1] = bad[2] = bad[3] = 0;
         fence_mbarrier_init();
@@ -437,62 +439,65 @@ segattn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_k, cons
         const int32_t next = *s_next;
         // quanta of the round (the last listed segment may end early), tiles, and this CTA's share
         const int32_t Q = a.quantum, slots = kTile / Q;
-        int32_t nq = 0;
+        int32_t nq = 0, cut_at = 0;                      // cut_at: the visible keys of the last quantum, when not all
         if (listed > 0) {
             const int32_t left = vmax - (w0 + list[listed - 1]) * g.seg, tail = (left + Q - 1) / Q;
             nq = (listed - 1) * a.per + (tail < a.per ? tail : a.per);
+            if (tail <= a.per) cut_at = left % Q;
         }
         const int32_t tiles = (nq + slots - 1) / slots;
         const int32_t mine = tiles > rank ? (tiles - rank + C - 1) / C : 0;
+        const int32_t cut_tile = cut_at > 0 && (tiles - 1) % C == rank ? mine - 1 : -1;
 
         if (warp < kSoftWarps) {
             // ------------------------------------------------------------ softmax
             if (first) {
-                // the queries into tensor memory, half a row per thread (rows without one: zeros)
+                // the queries to where the tensor core reads them, half a row per thread (rows
+                // without one: zeros)
                 uint4 qv[D / 16] = {};
                 if (used) {
                     const uint4 *src = reinterpret_cast<const uint4 *>(a.q + at * D + side * (D / 2));
 #pragma unroll
                     for (int e = 0; e < D / 16; ++e) qv[e] = src[e];
                 }
+                if constexpr (L::QT) {
 #pragma unroll
-                for (int c = 0; c < D / 64; ++c) {
-                    uint32_t w[16];
+                    for (int c = 0; c < D / 64; ++c) {
+                        uint32_t w[16];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        w[4 * e] = qv[4 * c + e].x, w[4 * e + 1] = qv[4 * c + e].y, w[4 * e + 2] = qv[4 * c + e].z,
-                              w[4 * e + 3] = qv[4 * c + e].w;
-                    tmem_st16(tmem + kColQ + side * (D / 4) + 16 * c + tlane, w);
+                        for (int e = 0; e < 4; ++e)
+                            w[4 * e] = qv[4 * c + e].x, w[4 * e + 1] = qv[4 * c + e].y, w[4 * e + 2] = qv[4 * c + e].z,
+                                  w[4 * e + 3] = qv[4 * c + e].w;
+                        tmem_st16(tmem + kColQ + side * (D / 4) + 16 * c + tlane, w);
+                    }
+                    tmem_st_wait();
+                } else {
+#pragma unroll
+                    for (int e = 0; e < D / 16; ++e)
+                        *reinterpret_cast<uint4 *>(base + L::Q + side * (kM * 128) + x * 128 + ((e ^ (x & 7)) << 4)) = qv[e];
+                    fence_proxy_async_smem();
                 }
-                tmem_st_wait();
                 tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(qfull);
             }
-            const int32_t vis = used ? svis[rl] : 0;
-            const int32_t word = rl >> 5, bit = rl & 31;
-            const uint64_t whole = Q == 64 ? ~0ull : (1ull << Q) - 1;
+            // which of a tile's keys the row takes
+            auto keys_of = [&](uint32_t t) {
+                wait_phase(&mfull[t % L::RING], (t / L::RING) & 1, g.status, abort_flag);
+                return used ? masks[t % L::RING * kM + rl] : 0;
+            };
+            uint64_t ahead = mine > 0 ? keys_of(u) : 0;
             for (int32_t k = 0; k < mine; ++k, ++u) {
-                const uint32_t sb = SB == 2 ? u & 1 : 0;
+                const uint32_t sb = u & 1;
                 const uint32_t ts = tmem + kColS + sb * kTile + tlane;
-                wait_phase(&mfull[u % kMetaRing], (u / kMetaRing) & 1, g.status, abort_flag);
-                uint64_t mask = 0;
-                int32_t cut = -1;                        // slot whose quantum ends behind the last visible key
-                int32_t cut_at = 0;
-                for (int32_t j = 0; j < slots; ++j) {
-                    const int2 d = meta[(u % kMetaRing) * 4 + j];
-                    if (d.y < 0) continue;
-                    if (d.y + Q > vmax) cut = j, cut_at = vmax - d.y;
-                    const int32_t c = vis - d.y;
-                    if (c > 0 && (used ? member[d.x + word] >> bit & 1u : 0u))
-                        mask |= (c >= Q ? whole : (1ull << c) - 1) << (j * Q);
-                }
-                wait_phase(&sfull[sb], (SB == 2 ? u >> 1 : u) & 1, g.status, abort_flag);
+                const uint64_t mask = ahead;
+                wait_phase(&sfull[sb], (u >> 1) & 1, g.status, abort_flag);
                 tc_fence_after_sync();
                 if (__any_sync(0xffffffffu, mask != 0)) {        // the same for both warps of a pair
                     uint32_t sq[2][16];
                     tmem_ld16(ts + side * 32, sq[0]);
                     tmem_ld16(ts + side * 32 + 16, sq[1]);
+                    if (k + 1 < mine) ahead = keys_of(u + 1);   // while the scores come
                     tmem_ld_wait16(sq[0]);
                     tmem_ld_wait16(sq[1]);
                     auto sv = [&](int j) -> uint32_t & { return sq[j >> 4][j & 15]; };
@@ -554,13 +559,14 @@ segattn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_k, cons
                 } else {
                     const uint32_t none[16] = {};
                     tmem_st16(ts + side * 16, none);
+                    if (k + 1 < mine) ahead = keys_of(u + 1);
                 }
                 tmem_st_wait();
-                if (cut >= 0) {
+                if (k == cut_tile) {
                     // values behind the last visible key: zeros
                     const uint32_t vs = u % NS;
                     wait_phase(&vfull[vs], (u / NS) & 1, g.status, abort_flag);
-                    const int r0 = cut * Q + cut_at, rows = (cut + 1) * Q - r0;
+                    const int r0 = (nq - 1) % slots * Q + cut_at, rows = Q - cut_at;
                     for (int e = tid; e < rows * (D / 8); e += 32 * kSoftWarps) {
                         const int r = r0 + e / (D / 8), ch = e % (D / 8);
                         *reinterpret_cast<uint4 *>(base + L::V + vs * L::STAGE + (ch >> 3) * kPlane + r * 128 +
@@ -575,8 +581,25 @@ segattn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_k, cons
         } else if (warp == kSoftWarps) {
             // ------------------------------------------------------------ copies
             const bool paged = g.layout_kv == LI_PA_BSND;
+            const uint64_t whole = Q == 64 ? ~0ull : (1ull << Q) - 1;
             const int32_t batch = 32 / slots;            // tiles whose slots the warp's lanes hold
             int32_t mb = 0, t0 = -1, c1 = 0, c2 = a.no_page;
+            // keys go a tile ahead of values, as the scores do
+            auto values = [&](uint32_t t, bool my, int32_t v1, int32_t v2) {
+                const uint32_t st = t % NS;
+                wait_phase(&vempty[st], ((t / NS) & 1) ^ 1u, g.status, abort_flag);
+                __syncwarp();
+                if (lane == 0) mbar_arrive_expect_tx(&vfull[st], L::STAGE);
+                __syncwarp();
+                if (my) {
+#pragma unroll
+                    for (int p = 0; p < D / 64; ++p)
+                        tma_load_3d(base + L::V + st * L::STAGE + p * kPlane + lane % slots * Q * 128, &map_v, &vfull[st],
+                                    n * D + 64 * p, v1, v2);
+                }
+            };
+            bool v_my = false;
+            int32_t v1 = 0, v2 = 0;
             for (int32_t k = 0; k < mine; ++k, ++u) {
                 const int32_t j = k % batch;
                 if (j == 0) {
@@ -606,14 +629,8 @@ segattn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_k, cons
                 const int32_t slot = lane % slots;
                 const uint32_t st = u % NS, ph = ((u / NS) & 1) ^ 1u;
                 wait_phase(&kempty[st], ph, g.status, abort_flag);
-                // the entry's last reader, the softmax of tile u - 8, finished before
-                // the scores of a tile that this key stage has held since were issued
-                if (my) meta[(u % kMetaRing) * 4 + slot] = make_int2(mb, t0);
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&mfull[u % kMetaRing]);
-                    mbar_arrive_expect_tx(&kfull[st], L::STAGE);
-                }
+                if (lane == 0) mbar_arrive_expect_tx(&kfull[st], L::STAGE);
                 __syncwarp();
                 if (my) {
 #pragma unroll
@@ -621,16 +638,26 @@ segattn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_k, cons
                         tma_load_3d(base + L::K + st * L::STAGE + p * kPlane + slot * Q * 128, &map_k, &kfull[st],
                                     n * D + 64 * p, c1, c2);
                 }
-                wait_phase(&vempty[st], ph, g.status, abort_flag);
-                if (lane == 0) mbar_arrive_expect_tx(&vfull[st], L::STAGE);
-                __syncwarp();
-                if (my) {
-#pragma unroll
-                    for (int p = 0; p < D / 64; ++p)
-                        tma_load_3d(base + L::V + st * L::STAGE + p * kPlane + slot * Q * 128, &map_v, &vfull[st],
-                                    n * D + 64 * p, c1, c2);
+                // the rows' masks; the entry's last reader, the softmax of tile u - RING, was
+                // done before the scores that this key stage has held since were issued
+                for (int32_t i = 0; i < MW; ++i) {
+                    const int32_t vis = svis[32 * i + lane];
+                    uint64_t m = 0;
+                    for (int32_t s = 0; s < slots; ++s) {
+                        const int32_t from = __shfl_sync(0xffffffffu, t0, j * slots + s);
+                        const int32_t at = __shfl_sync(0xffffffffu, mb, j * slots + s);
+                        if (from < 0) continue;
+                        const int32_t c = vis - from;
+                        if (c > 0 && (member[at + i] >> lane & 1u)) m |= (c >= Q ? whole : (1ull << c) - 1) << (s * Q);
+                    }
+                    masks[u % L::RING * kM + 32 * i + lane] = m;
                 }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&mfull[u % L::RING]);
+                if (k > 0) values(u - 1, v_my, v1, v2);
+                v_my = my, v1 = c1, v2 = c2;
             }
+            if (mine > 0) values(u - 1, v_my, v1, v2);
         } else {
             // ------------------------------------------------------------ products
             // (the whole warp runs the loop and one lane issues: addresses and
@@ -640,10 +667,11 @@ segattn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_k, cons
             const uint32_t id_s = make_idesc(fmt, fmt, kM, kTile);
             const uint32_t id_pv = make_idesc(fmt, fmt, kM, D) | (1u << 16);      // values MN-major
             const int32_t todo = __shfl_sync(0xffffffffu, mine, 0);
-            if (first) wait_phase(qfull, 0, g.status, abort_flag);   // the queries stand in tensor memory
+            if (first) wait_phase(qfull, 0, g.status, abort_flag);
+            const uint64_t qd = smem_desc_sw128(sbase + L::Q);
             auto weigh = [&](uint32_t t) {               // O += P V of tile t
-                const uint32_t st = t % NS, sb = SB == 2 ? t & 1 : 0;
-                wait_phase(&pfull[sb], (SB == 2 ? t >> 1 : t) & 1, g.status, abort_flag);
+                const uint32_t st = t % NS, sb = t & 1;
+                wait_phase(&pfull[sb], (t >> 1) & 1, g.status, abort_flag);
                 wait_phase(&vfull[st], (t / NS) & 1, g.status, abort_flag);
                 tc_fence_after_sync();
                 __syncwarp();
@@ -659,26 +687,28 @@ segattn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_k, cons
                 __syncwarp();
             };
             for (int32_t k = 0; k < todo; ++k, ++u) {
-                const uint32_t st = u % NS, sb = SB == 2 ? u & 1 : 0;
+                const uint32_t st = u % NS, sb = u & 1;
                 wait_phase(&kfull[st], (u / NS) & 1, g.status, abort_flag);
                 // the buffer's last weights have been read
-                if (u >= SB) wait_phase(pvdone, (u - SB) & 1, g.status, abort_flag);
+                if (u >= 2) wait_phase(pvdone, u & 1, g.status, abort_flag);
                 tc_fence_after_sync();
                 __syncwarp();
                 if (leader) {
                     const uint64_t kd = smem_desc_sw128(sbase + L::K + st * L::STAGE);
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk)
-                        mma_f16_ta(tmem + kColS + sb * kTile, tmem + kColQ + 8 * kk,
-                                   kd + ((kk >> 2) * kPlane + (kk & 3) * 32) / 16, id_s, kk != 0);
+                        if constexpr (L::QT)
+                            mma_f16_ta(tmem + kColS + sb * kTile, tmem + kColQ + 8 * kk, kd + kk * 2, id_s, kk != 0);
+                        else
+                            mma_f16(tmem + kColS + sb * kTile, qd + ((kk >> 2) * (kM * 128) + (kk & 3) * 32) / 16,
+                                    kd + ((kk >> 2) * kPlane + (kk & 3) * 32) / 16, id_s, kk != 0);
                     mma_commit(&sfull[sb]);
                     mma_commit(&kempty[st]);
                 }
                 __syncwarp();
-                if (SB == 1) weigh(u);
-                else if (k > 0) weigh(u - 1);
+                if (k > 0) weigh(u - 1);
             }
-            if (SB == 2 && todo > 0) weigh(u - 1);
+            if (todo > 0) weigh(u - 1);
             // a barrier of its own for the end: whoever waits for it late must not
             // take a later phase of pvdone for an earlier one
             if (next == kNone && leader) mma_commit(odone);
