@@ -379,32 +379,53 @@ def indexer(params: Params, query, key, weights, *, act_seq_q=None, act_seq_k=No
 
 # ---------------------------------------------------------------- rotary positions
 
-def _check_tensors(dev, **named):
-    """Device, type, size and contiguity of call arguments: name=(tensor, dtype, numel or None)."""
-    for name, (t, dtype, numel) in named.items():
-        if t.device != dev:
-            raise ValueError("%s is on %s, the call's other tensors on %s" % (name, t.device, dev))
-        if t.dtype != dtype:
-            raise TypeError("%s must be %s, not %s" % (name, dtype, t.dtype))
-        if numel is not None and (t.numel() != numel or not t.is_contiguous()):
-            raise ValueError("%s must be contiguous with %d elements, not %s" % (name, numel, tuple(t.shape)))
+_torch = None
+
+
+def _load_torch():
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
+def _arg(name, t, index, dtype, numel):
+    """Pointer of a tensor argument, after its checks: on device `index`, of
+    `dtype`, contiguous with `numel` elements (None: strides and size are the
+    caller's)."""
+    if t.get_device() != index:
+        raise ValueError("%s is on %s, the call's first tensor on %s"
+                         % (name, t.device, "cuda:%d" % index if index >= 0 else "the host"))
+    if t.dtype is not dtype:
+        raise TypeError("%s must be %s, not %s" % (name, dtype, t.dtype))
+    if numel is not None and (t.numel() != numel or not t.is_contiguous()):
+        raise ValueError("%s must be contiguous with %d elements, not %s" % (name, numel, tuple(t.shape)))
+    return t.data_ptr()
+
+
+def _opt(name, t, index, dtype, numel):
+    return None if t is None else _arg(name, t, index, dtype, numel)
 
 
 def _torch_dtype(code):
-    import torch
-    return {0: torch.bfloat16, 1: torch.float16, 2: torch.float32}[code]
+    torch = _load_torch()
+    return torch.bfloat16 if code == 0 else torch.float16 if code == 1 else torch.float32
 
 
-def _launch(dev, f, *args, stream=None):
-    """Call a library function for tensors on `dev`: current device and stream are its."""
-    import torch
-    if dev.type != "cuda":
-        raise ValueError("the call's tensors must be on a CUDA device, not on %s" % dev)
-    if dev.index is None or dev.index == torch.cuda.current_device():
-        _check(f(*args, _stream(stream)))
+def _launch(index, f, *args, stream=None):
+    """Call a library function for tensors on CUDA device `index`: the current
+    device and stream are that device's."""
+    torch = _torch
+    if index < 0:
+        raise ValueError("the call's tensors must be on a CUDA device")
+    if index == torch._C._cuda_getDevice():
+        st = f(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream))
     else:
-        with torch.cuda.device(dev):
-            _check(f(*args, _stream(stream)))
+        with torch.cuda.device(index):
+            st = f(*args, _stream(stream))
+    if st:
+        _check(st)
 
 
 def make_rope_params(problem=None, **kw) -> RopeParams:
@@ -443,20 +464,23 @@ def rope(params: RopeParams, positions, inv_freq, query, key=None, *, out=None, 
     """Rotate query [.., N1, D] and key [.., N2, D] by their rows' positions,
     allocating dense outputs unless they are given (query and key themselves for
     in place).  Returns (out, key_out or None)."""
-    import torch
-    dev, dt, p = query.device, _torch_dtype(params.dtype), params
-    _check_tensors(dev, positions=(positions, torch.int32, p.rows), inv_freq=(inv_freq, torch.float64, p.rot_dim // 2),
-                   query=(query, dt, None if p.q_row_stride or p.q_head_stride else p.rows * p.N1 * p.D))
+    torch = _load_torch()
+    p, d, dt = params, query.get_device(), _torch_dtype(params.dtype)
+    rows, D = p.rows, p.D
+    nq = rows * p.N1 * D
+    q = _arg("query", query, d, dt, None if p.q_row_stride or p.q_head_stride else nq)
     if out is None:
-        out = torch.empty((p.rows, p.N1, p.D), dtype=dt, device=dev)
-    _check_tensors(dev, out=(out, dt, None if p.q_out_row_stride or p.q_out_head_stride else p.rows * p.N1 * p.D))
+        out = torch.empty((rows, p.N1, D), dtype=dt, device=query.device)
+    o = _arg("out", out, d, dt, None if p.q_out_row_stride or p.q_out_head_stride else nq)
+    k = ko = None
     if key is not None:
         if key_out is None:
-            key_out = torch.empty((p.rows, p.N2, p.D), dtype=dt, device=dev)
-        _check_tensors(dev, key=(key, dt, None if p.k_row_stride or p.k_head_stride else p.rows * p.N2 * p.D),
-                       key_out=(key_out, dt, None if p.k_out_row_stride or p.k_out_head_stride else p.rows * p.N2 * p.D))
-    _launch(dev, lib().li_rope, ctypes.byref(p), positions.data_ptr(), inv_freq.data_ptr(), query.data_ptr(), _ptr(key),
-            out.data_ptr(), _ptr(key_out), stream=stream)
+            key_out = torch.empty((rows, p.N2, D), dtype=dt, device=query.device)
+        nk = rows * p.N2 * D
+        k = _arg("key", key, d, dt, None if p.k_row_stride or p.k_head_stride else nk)
+        ko = _arg("key_out", key_out, d, dt, None if p.k_out_row_stride or p.k_out_head_stride else nk)
+    _launch(d, lib().li_rope, ctypes.byref(p), _arg("positions", positions, d, torch.int32, rows),
+            _arg("inv_freq", inv_freq, d, torch.float64, p.rot_dim // 2), q, k, o, ko, stream=stream)
     return out, key_out
 
 
@@ -473,12 +497,15 @@ def page_pools(pools):
         return pools
     arr = (PagePool * len(pools))()
     for d, t in zip(arr, pools):
-        es = t.element_size()
-        if t.dim() < 1 or (t.shape[0] and not t[0].is_contiguous()):
+        if t.dim() < 1:
+            raise ValueError("a pool needs the page as its axis 0")
+        es, n = t.element_size(), t.shape[0]
+        each = t.numel() // n if n else 0
+        if n and not t.is_contiguous() and not t[0].is_contiguous():
             raise ValueError("a pool's pages must be contiguous")
         d.base = t.data_ptr()
-        d.page_bytes = (t[0].numel() if t.shape[0] else 0) * es
-        d.page_stride = max(t.stride(0) * es, d.page_bytes)
+        d.page_bytes = each * es
+        d.page_stride = max(t.stride(0) * es, each * es)
     arr.tensors = list(pools)
     return arr
 
@@ -494,84 +521,78 @@ def alloc_pages_workspace(params: PagesParams, device="cuda"):
     return torch.empty(li_pages_workspace_size(params), dtype=torch.uint8, device=device)
 
 
-def _pools_on(pools, params, dev):
+def _pools_on(pools, params, index):
     arr = page_pools(pools)
     for t in getattr(arr, "tensors", ()):
-        if t.device != dev:
-            raise ValueError("a pool is on %s, the call's other tensors on %s" % (t.device, dev))
+        if t.get_device() != index:
+            raise ValueError("a pool is on %s, the call's other tensors on cuda:%d" % (t.device, index))
         if t.shape[0] != params.num_pages:
             raise ValueError("a pool has %d pages, not %d" % (t.shape[0], params.num_pages))
     return arr
 
 
-def _pages_state(params, table, lens, refs, out, workspace, rows=()):
-    """Checks the state, allocates what is not given; returns (dev, out, workspace)."""
-    import torch
-    p, i32 = params, torch.int32
-    dev = table.device
+def _pages_state(params, table, lens, refs, out, workspace, status):
+    """Checks the state, allocates what is not given; returns (device index, out,
+    pointers of the state, of the outputs, of status and the workspace)."""
+    torch = _load_torch()
+    p, i32, d = params, torch.int32, table.get_device()
+    B, pages = p.B, p.num_pages
+    n = B * p.max_pages_per_seq
     if out is None:
         out = (torch.empty_like(table), torch.empty_like(lens), torch.empty_like(refs))
     if workspace is None:
-        workspace = alloc_pages_workspace(p, dev)
-    n = p.B * p.max_pages_per_seq
-    _check_tensors(dev, table=(table, i32, n), lens=(lens, i32, p.B), refs=(refs, i32, p.num_pages),
-                   table_out=(out[0], i32, n), lens_out=(out[1], i32, p.B), refs_out=(out[2], i32, p.num_pages),
-                   workspace=(workspace, torch.uint8, None))
-    for name, t, numel in rows:
-        _check_tensors(dev, **{name: (t, i32, numel)})
-    return dev, out, workspace
+        workspace = alloc_pages_workspace(p, table.device)
+    state = _arg("table", table, d, i32, n), _arg("lens", lens, d, i32, B), _arg("refs", refs, d, i32, pages)
+    after = (_arg("table_out", out[0], d, i32, n), _arg("lens_out", out[1], d, i32, B),
+             _arg("refs_out", out[2], d, i32, pages))
+    return d, out, state, after, (_opt("status", status, d, i32, 1), _arg("workspace", workspace, d, torch.uint8, None),
+                                  workspace.numel())
 
 
 def pages_copy(params: PagesParams, pools, src, dst, *, status=None, stream=None):
     """li_pages_copy: page src[i] -> page dst[i] of every pool (int32 tensors)."""
-    import torch
-    dev, n = src.device, src.numel()
-    _check_tensors(dev, src=(src, torch.int32, n), dst=(dst, torch.int32, n))
-    arr = _pools_on(pools, params, dev)
-    _launch(dev, lib().li_pages_copy, ctypes.byref(params), arr, len(arr), src.data_ptr(), dst.data_ptr(), n,
-            _ptr(status), stream=stream)
+    i32 = _load_torch().int32
+    d, n = src.get_device(), src.numel()
+    s, t = _arg("src", src, d, i32, n), _arg("dst", dst, d, i32, n)
+    arr = _pools_on(pools, params, d)
+    _launch(d, lib().li_pages_copy, ctypes.byref(params), arr, len(arr), s, t, n, _opt("status", status, d, i32, 1),
+            stream=stream)
 
 
 def pages_reserve(params: PagesParams, table, lens, refs, new_lens, *, out=None, workspace=None, status=None, stream=None):
     """li_pages_reserve.  Returns (table, lens, refs) after the call: new
     tensors, or `out` (which may be the inputs, for in place)."""
-    dev, out, ws = _pages_state(params, table, lens, refs, out, workspace, [("new_lens", new_lens, params.B)])
-    _launch(dev, lib().li_pages_reserve, ctypes.byref(params), table.data_ptr(), lens.data_ptr(), refs.data_ptr(),
-            new_lens.data_ptr(), out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), _ptr(status), ws.data_ptr(),
-            ws.numel(), stream=stream)
+    d, out, state, after, rest = _pages_state(params, table, lens, refs, out, workspace, status)
+    _launch(d, lib().li_pages_reserve, ctypes.byref(params), *state, _arg("new_lens", new_lens, d, _torch.int32, params.B),
+            *after, *rest, stream=stream)
     return out
 
 
 def pages_fork(params: PagesParams, pools, table, lens, refs, src_rows, dst_rows, *, out=None, workspace=None,
                status=None, stream=None):
     """li_pages_fork: row dst_rows[i] becomes a child of row src_rows[i]."""
-    n = src_rows.numel()
-    dev, out, ws = _pages_state(params, table, lens, refs, out, workspace,
-                                [("src_rows", src_rows, n), ("dst_rows", dst_rows, n)])
-    arr = _pools_on(pools, params, dev)
-    _launch(dev, lib().li_pages_fork, ctypes.byref(params), arr, len(arr), table.data_ptr(), lens.data_ptr(),
-            refs.data_ptr(), src_rows.data_ptr(), dst_rows.data_ptr(), n, out[0].data_ptr(), out[1].data_ptr(),
-            out[2].data_ptr(), _ptr(status), ws.data_ptr(), ws.numel(), stream=stream)
+    d, out, state, after, rest = _pages_state(params, table, lens, refs, out, workspace, status)
+    n, i32 = src_rows.numel(), _torch.int32
+    s, t = _arg("src_rows", src_rows, d, i32, n), _arg("dst_rows", dst_rows, d, i32, n)
+    arr = _pools_on(pools, params, d)
+    _launch(d, lib().li_pages_fork, ctypes.byref(params), arr, len(arr), *state, s, t, n, *after, *rest, stream=stream)
     return out
 
 
 def pages_free(params: PagesParams, table, lens, refs, rows, *, out=None, workspace=None, status=None, stream=None):
     """li_pages_free: empties the rows `rows` (int32)."""
+    d, out, state, after, rest = _pages_state(params, table, lens, refs, out, workspace, status)
     n = rows.numel()
-    dev, out, ws = _pages_state(params, table, lens, refs, out, workspace, [("rows", rows, n)])
-    _launch(dev, lib().li_pages_free, ctypes.byref(params), table.data_ptr(), lens.data_ptr(), refs.data_ptr(),
-            rows.data_ptr(), n, out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), _ptr(status), ws.data_ptr(),
-            ws.numel(), stream=stream)
+    _launch(d, lib().li_pages_free, ctypes.byref(params), *state, _arg("rows", rows, d, _torch.int32, n), n, *after, *rest,
+            stream=stream)
     return out
 
 
 def pages_compact(params: PagesParams, pools, table, lens, refs, *, out=None, workspace=None, status=None, stream=None):
     """li_pages_compact: the live pages become the first ones of the pool."""
-    dev, out, ws = _pages_state(params, table, lens, refs, out, workspace)
-    arr = _pools_on(pools, params, dev)
-    _launch(dev, lib().li_pages_compact, ctypes.byref(params), arr, len(arr), table.data_ptr(), lens.data_ptr(),
-            refs.data_ptr(), out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), _ptr(status), ws.data_ptr(),
-            ws.numel(), stream=stream)
+    d, out, state, after, rest = _pages_state(params, table, lens, refs, out, workspace, status)
+    arr = _pools_on(pools, params, d)
+    _launch(d, lib().li_pages_compact, ctypes.byref(params), arr, len(arr), *state, *after, *rest, stream=stream)
     return out
 
 
@@ -605,17 +626,15 @@ def _segment_keys(p):
     return (p.B * p.S2 if p.layout_kv == 0 else p.T2) * p.N2 * p.D
 
 
-def _segment_lens(p, dev, act_seq_q, act_seq_k, block_table, status):
-    import torch
-    i32 = torch.int32
-    if act_seq_q is not None:
-        _check_tensors(dev, act_seq_q=(act_seq_q, i32, p.B))
-    if act_seq_k is not None:
-        _check_tensors(dev, act_seq_k=(act_seq_k, i32, p.B))
-    if block_table is not None and p.layout_kv == 2:
-        _check_tensors(dev, block_table=(block_table, i32, p.B * p.max_blocks_per_seq))
-    if status is not None:
-        _check_tensors(dev, status=(status, i32, 1))
+def _segment_lens(p, index, act_seq_q, act_seq_k, block_table, status):
+    """Pointers of the lengths, the block table and status, after their checks."""
+    i32, B = _torch.int32, p.B
+    table = None
+    if block_table is not None:
+        table = (_arg("block_table", block_table, index, i32, B * p.max_blocks_per_seq) if p.layout_kv == 2
+                 else block_table.data_ptr())
+    return (_opt("act_seq_q", act_seq_q, index, i32, B), _opt("act_seq_k", act_seq_k, index, i32, B), table,
+            _opt("status", status, index, i32, 1))
 
 
 def segment_pool(params: SegmentParams, key, *, act_seq_k=None, block_table=None, first=None, pooled=None, status=None,
@@ -624,19 +643,16 @@ def segment_pool(params: SegmentParams, key, *, act_seq_k=None, block_table=None
     `first` (int32 [B]) and `pooled` only the segments of the tokens from there
     on are refreshed; segments behind a sequence keep what `pooled` holds
     (undefined in a newly allocated one)."""
-    import torch
-    p, dev = params, key.device
+    torch = _load_torch()
+    p, d = params, key.get_device()
+    k = _arg("key", key, d, _torch_dtype(p.dtype), _segment_keys(p))
     if pooled is None:
         if first is not None:
             raise ValueError("first refreshes an existing pooled tensor: pass pooled")
-        pooled = torch.empty((p.B, p.max_segs, p.N2, p.D), dtype=torch.float32, device=dev)
-    _segment_lens(p, dev, None, act_seq_k, block_table, status)
-    _check_tensors(dev, key=(key, _torch_dtype(p.dtype), _segment_keys(p)),
-                   pooled=(pooled, torch.float32, p.B * p.max_segs * p.N2 * p.D))
-    if first is not None:
-        _check_tensors(dev, first=(first, torch.int32, p.B))
-    _launch(dev, lib().li_segment_pool, ctypes.byref(p), key.data_ptr(), _ptr(act_seq_k), _ptr(block_table), _ptr(first),
-            pooled.data_ptr(), _ptr(status), stream=stream)
+        pooled = torch.empty((p.B, p.max_segs, p.N2, p.D), dtype=torch.float32, device=key.device)
+    _, lens, table, st = _segment_lens(p, d, None, act_seq_k, block_table, status)
+    _launch(d, lib().li_segment_pool, ctypes.byref(p), k, lens, table, _opt("first", first, d, torch.int32, p.B),
+            _arg("pooled", pooled, d, torch.float32, p.B * p.max_segs * p.N2 * p.D), st, stream=stream)
     return pooled
 
 
@@ -644,17 +660,15 @@ def segment_select(params: SegmentParams, query, pooled, *, act_seq_q=None, act_
                    stream=None):
     """li_segment_select: the chosen segments of each row and key head, int32
     [rows, N2, seg_count], ascending, -1 behind them."""
-    import torch
-    p, dev = params, query.device
-    rows = _segment_rows(p)
+    torch = _load_torch()
+    p, d = params, query.get_device()
+    rows, N2, D, count = _segment_rows(p), p.N2, p.D, p.seg_count
+    q = _arg("query", query, d, _torch_dtype(p.dtype), rows * p.N1 * D)
     if out is None:
-        out = torch.empty((rows, p.N2, p.seg_count), dtype=torch.int32, device=dev)
-    _segment_lens(p, dev, act_seq_q, act_seq_k, None, status)
-    _check_tensors(dev, query=(query, _torch_dtype(p.dtype), rows * p.N1 * p.D),
-                   pooled=(pooled, torch.float32, p.B * p.max_segs * p.N2 * p.D),
-                   out=(out, torch.int32, rows * p.N2 * p.seg_count))
-    _launch(dev, lib().li_segment_select, ctypes.byref(p), query.data_ptr(), pooled.data_ptr(), _ptr(act_seq_q),
-            _ptr(act_seq_k), out.data_ptr(), _ptr(status), stream=stream)
+        out = torch.empty((rows, N2, count), dtype=torch.int32, device=query.device)
+    q_lens, k_lens, _, st = _segment_lens(p, d, act_seq_q, act_seq_k, None, status)
+    _launch(d, lib().li_segment_select, ctypes.byref(p), q, _arg("pooled", pooled, d, torch.float32, p.B * p.max_segs * N2 * D),
+            q_lens, k_lens, _arg("out", out, d, torch.int32, rows * N2 * count), st, stream=stream)
     return out
 
 
@@ -662,19 +676,17 @@ def segment_attention(params: SegmentParams, query, key, value, seg_idx, *, act_
                       block_table=None, out=None, lse=None, want_lse=True, status=None, stream=None):
     """li_segment_attention, allocating out [rows, N1, D] (the query's dtype) and,
     when asked, lse [rows, N1] fp32.  Returns (out, lse or None)."""
-    import torch
-    p, dev, dt = params, query.device, _torch_dtype(params.dtype)
-    rows, keys = _segment_rows(p), _segment_keys(p)
+    torch = _load_torch()
+    p, d, dt = params, query.get_device(), _torch_dtype(params.dtype)
+    rows, keys, N1, D = _segment_rows(p), _segment_keys(p), p.N1, p.D
+    n = rows * N1 * D
+    q, k, v = (_arg("query", query, d, dt, n), _arg("key", key, d, dt, keys), _arg("value", value, d, dt, keys))
     if out is None:
-        out = torch.empty((rows, p.N1, p.D), dtype=dt, device=dev)
+        out = torch.empty((rows, N1, D), dtype=dt, device=query.device)
     if lse is None and want_lse:
-        lse = torch.empty((rows, p.N1), dtype=torch.float32, device=dev)
-    _segment_lens(p, dev, act_seq_q, act_seq_k, block_table, status)
-    _check_tensors(dev, query=(query, dt, rows * p.N1 * p.D), key=(key, dt, keys), value=(value, dt, keys),
-                   seg_idx=(seg_idx, torch.int32, rows * p.N2 * p.seg_count), out=(out, dt, rows * p.N1 * p.D))
-    if lse is not None:
-        _check_tensors(dev, lse=(lse, torch.float32, rows * p.N1))
-    _launch(dev, lib().li_segment_attention, ctypes.byref(p), query.data_ptr(), key.data_ptr(), value.data_ptr(),
-            seg_idx.data_ptr(), _ptr(act_seq_q), _ptr(act_seq_k), _ptr(block_table), out.data_ptr(), _ptr(lse),
-            _ptr(status), stream=stream)
+        lse = torch.empty((rows, N1), dtype=torch.float32, device=query.device)
+    q_lens, k_lens, table, st = _segment_lens(p, d, act_seq_q, act_seq_k, block_table, status)
+    _launch(d, lib().li_segment_attention, ctypes.byref(p), q, k, v,
+            _arg("seg_idx", seg_idx, d, torch.int32, rows * p.N2 * p.seg_count), q_lens, k_lens, table,
+            _arg("out", out, d, dt, n), _opt("lse", lse, d, torch.float32, rows * N1), st, stream=stream)
     return out, lse
