@@ -1,5 +1,7 @@
 // li_segment.cu -- the cheap score of segment-sparse attention: the mean key of
 // each segment (pool) and the choice of segments for each query row (select).
+#include <cooperative_groups.h>
+
 #include <cmath>
 #include <cstdio>
 
@@ -123,7 +125,8 @@ using namespace li;
 
 constexpr int kPoolThreads = 256;
 constexpr int kSelThreads = 256;
-constexpr int kSelRows = 16;               // most query rows of one select block
+constexpr int kSelRows = 32;               // most query rows of one select block
+constexpr int kSelSplit = 8;               // most blocks of a cluster that shares a row's segments
 
 // ---------------------------------------------------------------------- pool
 
@@ -195,14 +198,22 @@ __global__ void __launch_bounds__(kPoolThreads) pool_kernel(const SegGeo g, cons
 
 // -------------------------------------------------------------------- select
 
-// A block takes R query rows and one key head.  Their scores stay in shared
-// memory: q (summed over the key head's query heads) and the products are held
-// in 64 bits, because the choice is by comparison and 32 bits would order
-// neighbours by rounding.  The products run on the 64-bit matrix instruction
-// (8 rows x 8 segments x 4 columns); a lane reads four neighbouring columns of
-// a segment's mean at once and the four steps take them in that order (a dot
-// product does not mind).  Then 256/R threads per row bisect for the score that
-// the last chosen segment has, and write the chosen ones in order.
+// The choice is by comparison, so it has to be that of scores in 64 bits; but
+// nearly every comparison is settled by far less.  The scores are first taken on
+// the 16-bit matrix instruction from q = qh + ql and P = ph + pl (two bf16 parts
+// each): qh.ph + qh.pl + ql.ph is off by at most E = 8 * 2^-16 |q| |P| (2^-16 for
+// the part dropped and for the rounding of each second part; the fp32 sums, 24
+// steps of 17 terms that lose 2^-23 each at the worst, 3.2 * 2^-16).  A row then bisects
+// for its last chosen score; when the gap to the first one left out is above 2E,
+// the choice is that of the exact scores.  Otherwise the scores within 2E of the
+// border (two or three of 500, in one row of six) are computed in 64 bits and
+// ranked; more than 32 of them (ties), and scores that are not finite, send the
+// row to a pass in 64 bits by the whole block.
+//
+// A block takes R rows and one key head, its warps 16 segments at a time; when
+// rows are few, a cluster of C blocks shares a row's segments and its first
+// block chooses.  Bound by L2 (each block reads its sequence's means) and by the
+// bisection, a dozen counts of a row's scores held in registers.
 
 struct SelArgs {
     SegGeo g;
@@ -212,59 +223,364 @@ struct SelArgs {
     int32_t R, ld;                         // rows per block; scores per row
 };
 
-__device__ __forceinline__ void mma_f64(double &d0, double &d1, double a, double b)
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint4 &a, uint32_t b0, uint32_t b1)
 {
-    asm volatile("mma.sync.aligned.m8n8k4.row.col.f64.f64.f64.f64 {%0, %1}, {%2}, {%3}, {%0, %1};"
-                 : "+d"(d0), "+d"(d1)
-                 : "d"(a), "d"(b));
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
 }
 
-// Order of the scores as unsigned integers (NaN lowest, -0 = +0).
+// Two numbers as their leading and following bf16 parts.
+__device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t &lo)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    hi = *reinterpret_cast<const uint32_t *>(&h);
+    const __nv_bfloat162 l = __floats2bfloat162_rn(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xFFFF0000u));
+    lo = *reinterpret_cast<const uint32_t *>(&l);
+}
+
+// Order of the scores as unsigned integers (-0 = +0; in 64 bits NaN lowest).
 __device__ __forceinline__ uint64_t order_of(double x)
 {
     if (x != x) return 0;
     const uint64_t u = (uint64_t)__double_as_longlong(x + 0.0);
     return u >> 63 ? ~u : u | 0x8000000000000000ull;
 }
-
-__device__ __forceinline__ void team_sync(int team, int threads)
+__device__ __forceinline__ uint32_t order_of(float x)      // NaN above inf; 0 is not used
 {
-    if (threads == 32) __syncwarp();
-    else asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(threads) : "memory");
+    uint32_t u = __float_as_uint(x);
+    u = u == 0x80000000u ? 0u : u;
+    return (u & 0x7FFFFFFFu) > 0x7F800000u ? 0xFFFFFFFFu : u >> 31 ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float value_of(uint32_t u) { return __uint_as_float(u >> 31 ? u & 0x7FFFFFFFu : ~u); }
+
+// q . P[s] in 64 bits, by a warp.
+template <int D>
+__device__ __forceinline__ double exact_score(const double *q, const float *P, int64_t ldp, int32_t s, int lane)
+{
+    double x = 0;
+    if (lane < D / 4) {
+        const float4 p = reinterpret_cast<const float4 *>(P + s * ldp)[lane];
+        const double2 a = reinterpret_cast<const double2 *>(q)[2 * lane], b = reinterpret_cast<const double2 *>(q)[2 * lane + 1];
+        x = a.x * p.x + a.y * p.y + b.x * p.z + b.y * p.w;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
 }
 
-template <int D, bool F16>
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const SelArgs a)
+// What a row chooses from and where it writes.
+struct SelRow {
+    const float *sc;                       // approximate scores
+    const double *q;
+    const float *P;
+    int64_t ldp;
+    int32_t *out;
+    int32_t ns, init, local, count;
+    float err;                             // E
+};
+
+struct SelShared {
+    int32_t sums[2][kSelThreads / 32];
+    uint32_t lows[kSelThreads / 32], highs[kSelThreads / 32];
+    int32_t band[kSelThreads / 32][32];    // segments near the border, per team
+    int32_t bands[kSelThreads / 32];
+    uint32_t taken[kSelThreads / 32];
+};
+
+// A team (one warp, or with WIDE the block) chooses for one row.  KR: scores per
+// thread in registers (0: read again in every pass).  Returns false when the
+// border cannot be settled here.
+template <int D, int KR, bool WIDE>
+__device__ bool choose(const SelRow &r, SelShared &sh, int team)
 {
-    constexpr int LDQ = D + 2;             // doubles per row: the 8 rows of a fragment hit different banks
+    constexpr int T = WIDE ? kSelThreads : 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = WIDE ? threadIdx.x : lane;
+    auto sync = [&]() {
+        if constexpr (WIDE) __syncthreads();
+        else __syncwarp();
+    };
+    int turn = 0;
+    auto sum = [&](int32_t v) {
+        v = __reduce_add_sync(0xffffffffu, v);
+        if constexpr (WIDE) {
+            if (lane == 0) sh.sums[turn][warp] = v;
+            __syncthreads();
+            v = 0;
+            for (int w = 0; w < kSelThreads / 32; ++w) v += sh.sums[turn][w];
+            turn ^= 1;
+        }
+        return v;
+    };
+    auto least = [&](uint32_t lo) {
+        lo = __reduce_min_sync(0xffffffffu, lo);
+        if constexpr (WIDE) {
+            __syncthreads();
+            if (lane == 0) sh.lows[warp] = lo;
+            __syncthreads();
+            for (int w = 0; w < kSelThreads / 32; ++w) lo = sh.lows[w] < lo ? sh.lows[w] : lo;
+        }
+        return lo;
+    };
+    auto most = [&](uint32_t hi) {
+        hi = __reduce_max_sync(0xffffffffu, hi);
+        if constexpr (WIDE) {
+            __syncthreads();
+            if (lane == 0) sh.highs[warp] = hi;
+            __syncthreads();
+            for (int w = 0; w < kSelThreads / 32; ++w) hi = sh.highs[w] > hi ? sh.highs[w] : hi;
+        }
+        return hi;
+    };
+    // scores as ordered integers; 0: not of the free choice [from, to)
+    const int32_t from = r.init, to = r.ns - r.local, need = r.count - r.init - r.local;
+    auto key_at = [&](int32_t s) -> uint32_t { return s >= from && s < to ? order_of(r.sc[s]) : 0u; };
+    uint32_t key[KR > 0 ? KR : 1];
+    if constexpr (KR > 0) {
+#pragma unroll
+        for (int k = 0; k < KR; ++k) key[k] = key_at(k * T + t);
+    }
+    auto each = [&](auto &&f) {                        // f(segment, key), all of the row's segments
+        if constexpr (KR > 0) {
+#pragma unroll
+            for (int k = 0; k < KR; ++k) f(k * T + t, key[k]);
+        } else {
+            for (int32_t s = t; s < r.ns; s += T) f(s, key_at(s));
+        }
+    };
+    // chosen: keys from `cut` on; with a band also the ones of it that are `taken`
+    uint32_t cut = 1, band_lo = 1, band_hi = 0, taken = 0;
+    int32_t ties = 0;                                  // equal scores of the cut that are chosen, lowest first (0: all)
+    if (need > 0) {
+        uint32_t lo = 0xffffffffu, hi = 0;
+        each([&](int32_t, uint32_t k) {
+            lo = k && k < lo ? k : lo;
+            hi = k > hi ? k : hi;
+        });
+        lo = least(lo);
+        hi = most(hi);
+        // not finite: the ordered integers of -inf, +inf and NaN lie outside
+        if (lo <= order_of(-INFINITY) || hi >= order_of(INFINITY) || !(r.err < INFINITY)) return false;
+        bool even = false;                             // exactly `need` scores from lo on
+        while (lo < hi && !even) {
+            const uint32_t mid = lo + ((hi - lo) >> 1) + ((hi - lo) & 1);
+            int32_t c = 0;
+            each([&](int32_t, uint32_t k) { c += k >= mid; });
+            c = sum(c);
+            if (c >= need) lo = mid;
+            else hi = mid - 1;
+            even = c == need;
+        }
+        cut = lo;
+        if (even) {
+            uint32_t in = 0xffffffffu, out = 0;
+            each([&](int32_t, uint32_t k) {
+                if (k >= cut) in = k < in ? k : in;
+                else out = k > out ? k : out;
+            });
+            cut = least(in);
+            out = most(out);
+            even = out == 0 || value_of(cut) - value_of(out) > 2.f * r.err;
+        }
+        if (!even) {
+            if (r.err == 0.f) {                        // every score is exact (zero): only ties
+                int32_t c = 0;
+                each([&](int32_t, uint32_t k) { c += k > cut; });
+                ties = need - sum(c);
+            } else {
+                const float v = value_of(cut);
+                band_lo = order_of(v - 2.f * r.err);
+                band_hi = order_of(v + 2.f * r.err);
+                int32_t above = 0, inside = 0;
+                each([&](int32_t, uint32_t k) {
+                    above += k > band_hi;
+                    inside += k >= band_lo && k <= band_hi;
+                });
+                above = sum(above);
+                inside = sum(inside);
+                if (inside > 32) return false;
+                if (t == 0) sh.bands[team] = 0;
+                sync();
+                each([&](int32_t s, uint32_t k) {
+                    if (k >= band_lo && k <= band_hi) sh.band[team][atomicAdd(&sh.bands[team], 1)] = s;
+                });
+                sync();
+                if (!WIDE || warp == 0) {              // one warp ranks them: score, then the lower segment
+                    double mine = 0;
+                    const int32_t s = lane < inside ? sh.band[team][lane] : 0;
+                    for (int i = 0; i < inside; ++i) {
+                        const double x = exact_score<D>(r.q, r.P, r.ldp, sh.band[team][i], lane);
+                        if (lane == i) mine = x;
+                    }
+                    const uint64_t ord = order_of(mine);
+                    int rank = 0;
+                    for (int i = 0; i < inside; ++i) {
+                        const uint64_t o = __shfl_sync(0xffffffffu, ord, i);
+                        const int32_t so = __shfl_sync(0xffffffffu, s, i);
+                        rank += o > ord || (o == ord && so < s);
+                    }
+                    const uint32_t m = __ballot_sync(0xffffffffu, lane < inside && rank < need - above);
+                    if (lane == 0) sh.taken[team] = m;
+                }
+                sync();
+                taken = sh.taken[team];
+                cut = band_hi + 1;
+            }
+        }
+    }
+    // in order: the forced ones, and the chosen
+    const uint32_t below = (1u << lane) - 1u;
+    int32_t done = 0, tied = 0;
+    auto place = [&](bool b, int32_t base, int32_t &total) {   // rank of this thread's among the team's in order
+        const uint32_t m = __ballot_sync(0xffffffffu, b);
+        int32_t rank = base + __popc(m & below);
+        total = __popc(m);
+        if constexpr (WIDE) {
+            if (lane == 0) sh.sums[turn][warp] = total;
+            __syncthreads();
+            total = 0;
+            for (int w = 0; w < kSelThreads / 32; ++w) {
+                if (w < warp) rank += sh.sums[turn][w];
+                total += sh.sums[turn][w];
+            }
+            turn ^= 1;
+        }
+        return rank;
+    };
+    auto step = [&](int32_t s, uint32_t k) {
+        bool in = s < r.ns && (k == 0 || (need > 0 && k >= cut));
+        if (k >= band_lo && k <= band_hi) {
+            in = false;
+            for (uint32_t m = taken; m; m &= m - 1) in |= sh.band[team][__ffs(m) - 1] == s;
+        }
+        int32_t total;
+        if (ties > 0) {
+            const int32_t rank = place(k == cut, tied, total);
+            if (k == cut && rank >= ties) in = false;
+            tied += total;
+        }
+        const int32_t rank = place(in, done, total);
+        if (in) r.out[rank] = s;
+        done += total;
+    };
+    if constexpr (KR > 0) {
+#pragma unroll
+        for (int k = 0; k < KR; ++k) step(k * T + t, key[k]);
+    } else {
+        for (int32_t s0 = 0; s0 < r.ns; s0 += T) step(s0 + t, s0 + t < r.ns ? key_at(s0 + t) : 0u);
+    }
+    return true;
+}
+
+// The same from scores in 64 bits, by the whole block (x: room for ns doubles).
+template <int D>
+__device__ void choose_exactly(const SelRow &r, SelShared &sh, double *x)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int32_t from = r.init, to = r.ns - r.local, need = r.count - r.init - r.local;
+    __syncthreads();
+    for (int32_t s = warp; s < r.ns; s += kSelThreads / 32) {
+        const double v = exact_score<D>(r.q, r.P, r.ldp, s, lane);
+        if (lane == 0) x[s] = v;
+    }
+    __syncthreads();
+    int turn = 0;
+    auto sum = [&](int32_t v, int32_t *before) {
+        v = __reduce_add_sync(0xffffffffu, v);
+        if (lane == 0) sh.sums[turn][warp] = v;
+        __syncthreads();
+        int32_t t = 0;
+        for (int w = 0; w < kSelThreads / 32; ++w) {
+            if (before && w < warp) *before += sh.sums[turn][w];
+            t += sh.sums[turn][w];
+        }
+        turn ^= 1;
+        return t;
+    };
+    // the largest threshold that at least `need` scores reach
+    uint64_t lo = 0, hi = ~0ull;
+    while (lo < hi) {
+        const uint64_t mid = lo + ((hi - lo) >> 1) + ((hi - lo) & 1);
+        int32_t c = 0;
+        for (int32_t s = from + tid; s < to; s += kSelThreads) c += order_of(x[s]) >= mid;
+        if (sum(c, nullptr) >= need) lo = mid;
+        else hi = mid - 1;
+    }
+    int32_t c = 0;
+    for (int32_t s = from + tid; s < to; s += kSelThreads) c += order_of(x[s]) > lo;
+    const int32_t ties = need - sum(c, nullptr);
+    int32_t done = 0, tied = 0;
+    for (int32_t s0 = 0; s0 < r.ns; s0 += kSelThreads) {
+        const int32_t s = s0 + tid;
+        bool in = s < r.ns, at = false;
+        if (in && s >= from && s < to) {
+            const uint64_t u = order_of(x[s]);
+            in = u > lo;
+            at = u == lo;
+        }
+        const uint32_t below = (1u << lane) - 1u;
+        uint32_t m = __ballot_sync(0xffffffffu, at);
+        int32_t rank = tied + __popc(m & below);
+        tied += sum(at, &rank);
+        in |= at && rank < ties;
+        m = __ballot_sync(0xffffffffu, in);
+        rank = done + __popc(m & below);
+        done += sum(in, &rank);
+        if (in) r.out[rank] = s;
+    }
+}
+
+template <int D, bool F16, int MT, int C>
+__global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelArgs a)
+{
+    constexpr int KS = D / 16;
     extern __shared__ double dyn[];
     const SegGeo &g = a.g;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int R = a.R, R8 = (R + 7) & ~7;
-    double *sq = dyn;                      // [R8][LDQ]
-    double *red = sq + R8 * LDQ;           // [256 / (R*D/8)][R][D] partial sums, then the scores
-    double *sc = red;                      // [R][ld]
+    const int R = a.R;
+    double *sq = dyn;                                          // [R][D]
+    uint4 *frag = reinterpret_cast<uint4 *>(sq + R * D);       // [MT][KS][2][32]: q's two parts as fragments
+    float *sc = reinterpret_cast<float *>(frag + MT * KS * 64);                   // [R][ld]
+    double *red = reinterpret_cast<double *>(sc + (C > 1 ? (size_t)(R > 2 ? R : 2) * a.ld : 0));   // partial sums of q
     __shared__ SegRow rows[kSelRows];
-    __shared__ int32_t warp_count[2][kSelThreads / 32];
-    const int32_t row0 = blockIdx.x * R, n = blockIdx.y;
+    __shared__ int32_t segs[kSelRows], most_segs;
+    __shared__ float qnorm[kSelRows];
+    __shared__ uint32_t pnorm[kSelRows], pbits[kSelRows];      // of a run's means: largest |P|^2, all bits; at its first row
+    __shared__ int32_t unsettled[kSelRows], unsettled_n;
+    __shared__ SelShared sh;
+    namespace cg = cooperative_groups;
+    const int rank = C > 1 ? (int)(blockIdx.x % C) : 0;
+    const int32_t row0 = (int32_t)(blockIdx.x / C) * R, n = blockIdx.y;
     const int nr = g.rows - row0 < R ? g.rows - row0 : R;
-    if (tid < R) {
+    if (warp == 0) {                       // R <= 32
         SegRow r{};
         r.b = -1;
-        if (tid < nr) r = seg_row(g, row0 + tid);
-        rows[tid] = r;
+        int32_t ns = 0;
+        if (lane < nr) {
+            r = seg_row(g, row0 + lane);
+            ns = (int32_t)(((uint32_t)r.vis + (uint32_t)g.seg - 1) / (uint32_t)g.seg);
+            if (ns > g.max_segs) {
+                ns = g.max_segs;
+                seg_flag(g, LI_DEV_BAD_KLEN);
+            }
+        }
+        if (lane < R) {
+            rows[lane] = r;
+            segs[lane] = ns;
+            pnorm[lane] = pbits[lane] = 0;
+        }
+        ns = __reduce_max_sync(0xffffffffu, ns);
+        if (lane == 0) {
+            most_segs = ns;
+            unsettled_n = 0;
+        }
     }
     __syncthreads();
-    auto segs_of = [&](const SegRow &r) {
-        const int32_t ns = (int32_t)(((int64_t)r.vis + g.seg - 1) / g.seg);
-        return ns > g.max_segs ? g.max_segs : ns;
-    };
-    int32_t most = 0;
-    for (int r = 0; r < nr; ++r) {
-        const int32_t ns = segs_of(rows[r]);
-        most = ns > most ? ns : most;
-        if (tid == 0 && ((int64_t)rows[r].vis + g.seg - 1) / g.seg > g.max_segs) seg_flag(g, LI_DEV_BAD_KLEN);
-    }
+    if constexpr (C > 1) cg::this_cluster().barrier_arrive();
+    auto means_of = [&](int32_t b) { return a.pooled + ((int64_t)b * g.max_segs * g.N2 + n) * D; };
+    const int64_t ldp = (int64_t)g.N2 * D;
+    const int32_t most = most_segs;
     if (most > g.count) {
         // ---- q summed over the heads of this key head
         const int per = R * (D / 8);       // threads that cover R rows once
@@ -287,7 +603,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelArgs a)
                 }
             }
             if (e < per && part < parts) {
-                double *dst = parts > 1 ? red + ((int64_t)part * R + r) * D + c : sq + r * LDQ + c;
+                double *dst = parts > 1 ? red + ((int64_t)part * R + r) * D + c : sq + r * D + c;
 #pragma unroll
                 for (int k = 0; k < 8; ++k) dst[k] = acc[k];
             }
@@ -297,163 +613,208 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelArgs a)
             for (int e = tid; e < R * D; e += kSelThreads) {
                 double acc = 0;
                 for (int k = 0; k < parts; ++k) acc += red[k * R * D + e];
-                sq[e / D * LDQ + e % D] = acc;
+                sq[e] = acc;
             }
+            __syncthreads();
         }
-        for (int e = R * LDQ + tid; e < R8 * LDQ; e += kSelThreads) sq[e] = 0;
+        // ---- its fragments: lane l of step k holds columns 16k + 4(l%4) .. + 3 of
+        // rows l/4 and l/4 + 8 (a dot product does not mind the order of columns)
+        for (int e = tid; e < MT * KS * 32; e += kSelThreads) {
+            const int l = e & 31, ks = (e >> 5) % KS, mt = (e >> 5) / KS;
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                const int r = mt * 16 + (l >> 2) + (h & 1) * 8, c = ks * 16 + 4 * (l & 3) + (h >> 1) * 2;
+                const double x = r < R ? sq[r * D + c] : 0, y = r < R ? sq[r * D + c + 1] : 0;
+                split2((float)x, (float)y, hi[h], lo[h]);
+            }
+            uint4 *dst = frag + (mt * KS + ks) * 64 + l;
+            dst[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            dst[32] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+        for (int r = warp; r < R; r += kSelThreads / 32) {
+            double x = 0;
+            for (int c = lane; c < D; c += 32) x = fma(sq[r * D + c], sq[r * D + c], x);
+#pragma unroll
+            for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+            if (lane == 0) qnorm[r] = x > 0 ? fmaxf((float)sqrt(x) * 1.0001f, 1e-30f) : (x == 0 ? 0.f : INFINITY);
+        }
         __syncthreads();
+        float *there = sc;                                     // where the scores go: the cluster's first block
+        if constexpr (C > 1) {
+            cg::this_cluster().barrier_wait();                 // it runs
+            there = cg::this_cluster().map_shared_rank(sc, 0);
+        }
         // ---- scores, one run of rows of the same batch after another
         for (int r0 = 0; r0 < nr;) {
             const int32_t b = rows[r0].b;
             int r1 = r0 + 1;
-            int32_t ns = segs_of(rows[r0]);
+            int32_t ns = segs[r0];
             while (r1 < nr && rows[r1].b == b) {
-                const int32_t m = segs_of(rows[r1]);
+                const int32_t m = segs[r1];
                 ns = m > ns ? m : ns;
                 ++r1;
             }
-            const float *P = a.pooled + ((int64_t)b * g.max_segs * g.N2 + n) * D;
-            const int64_t ldp = (int64_t)g.N2 * D;
-            for (int32_t s0 = warp * 8; s0 < ns; s0 += kSelThreads / 4) {
-                double acc[2][2] = {};
-                const int32_t s = s0 + (lane >> 2);
-                const float4 *src = reinterpret_cast<const float4 *>(P + (s < ns ? s : ns - 1) * ldp) + (lane & 3);
-                float4 p[D / 16];
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k) p[k] = src[4 * k];
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const double bv[4] = {p[k].x, p[k].y, p[k].z, p[k].w};
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        if (t * 8 >= R) break;
-                        const double2 *qa = reinterpret_cast<const double2 *>(sq + (t * 8 + (lane >> 2)) * LDQ + 16 * k + 4 * (lane & 3));
-                        const double2 q0 = qa[0], q1 = qa[1];
-                        mma_f64(acc[t][0], acc[t][1], q0.x, bv[0]);
-                        mma_f64(acc[t][0], acc[t][1], q0.y, bv[1]);
-                        mma_f64(acc[t][0], acc[t][1], q1.x, bv[2]);
-                        mma_f64(acc[t][0], acc[t][1], q1.y, bv[3]);
-                    }
-                }
-                // lane: row lane/4, segments s0 + 2*(lane%4) and the next
+            const float *P = means_of(b);
+            float norm = 0.f;
+            uint32_t bits = 0;
+            for (int32_t s0 = (rank * (kSelThreads / 32) + warp) * 16; s0 < ns; s0 += C * (kSelThreads / 32) * 16) {
+                float4 p[2][KS];
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
-                    const int r = t * 8 + (lane >> 2);
-                    const int32_t c = s0 + 2 * (lane & 3);
-                    if (r >= r0 && r < r1) {
-                        if (c < ns) sc[(int64_t)r * a.ld + c] = acc[t][0];
-                        if (c + 1 < ns) sc[(int64_t)r * a.ld + c + 1] = acc[t][1];
+                    const int32_t s = s0 + 8 * t + (lane >> 2);
+                    const float4 *src = reinterpret_cast<const float4 *>(P + (s < ns ? s : ns - 1) * ldp) + (lane & 3);
+#pragma unroll
+                    for (int k = 0; k < KS; ++k) p[t][k] = src[4 * k];
+                }
+                float acc[MT][2][4] = {};
+#pragma unroll
+                for (int k = 0; k < KS; ++k) {
+                    uint32_t hi[2][2], lo[2][2];
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        split2(p[t][k].x, p[t][k].y, hi[t][0], lo[t][0]);
+                        split2(p[t][k].z, p[t][k].w, hi[t][1], lo[t][1]);
+                    }
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) {
+                        const uint4 qh = frag[(m * KS + k) * 64 + lane], ql = frag[(m * KS + k) * 64 + 32 + lane];
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            mma_bf16(acc[m][t], ql, hi[t][0], hi[t][1]);
+                            mma_bf16(acc[m][t], qh, lo[t][0], lo[t][1]);
+                            mma_bf16(acc[m][t], qh, hi[t][0], hi[t][1]);
+                        }
                     }
                 }
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    float x = 0.f;
+#pragma unroll
+                    for (int k = 0; k < KS; ++k) {
+                        const float4 v = p[t][k];
+                        x = fmaf(v.x, v.x, fmaf(v.y, v.y, fmaf(v.z, v.z, fmaf(v.w, v.w, x))));
+                        bits |= __float_as_uint(v.x) | __float_as_uint(v.y) | __float_as_uint(v.z) | __float_as_uint(v.w);
+                    }
+                    x += __shfl_xor_sync(0xffffffffu, x, 1);
+                    x += __shfl_xor_sync(0xffffffffu, x, 2);
+                    norm = fmaxf(norm, x);
+                    // lane: rows lane/4 and lane/4 + 8, segments s0 + 8t + 2*(lane%4) and the next
+                    const int32_t c = s0 + 8 * t + 2 * (lane & 3);
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int r = m * 16 + (lane >> 2) + 8 * h;
+                            if (r >= r0 && r < r1) {
+                                if (c < ns) there[(int64_t)r * a.ld + c] = acc[m][t][2 * h];
+                                if (c + 1 < ns) there[(int64_t)r * a.ld + c + 1] = acc[m][t][2 * h + 1];
+                            }
+                        }
+                }
+            }
+            const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(norm));   // (>= 0: ordered as integers)
+            bits = __reduce_or_sync(0xffffffffu, bits & 0x7FFFFFFFu);
+            if (lane == 0) {
+                uint32_t *to_n = pnorm + r0, *to_b = pbits + r0;
+                if constexpr (C > 1) {
+                    to_n = cg::this_cluster().map_shared_rank(to_n, 0);
+                    to_b = cg::this_cluster().map_shared_rank(to_b, 0);
+                }
+                atomicMax(to_n, top);
+                atomicOr(to_b, bits);
             }
             r0 = r1;
         }
+        if constexpr (C > 1) {
+            cg::this_cluster().sync();
+            if (rank != 0) return;
+        }
         __syncthreads();
+    } else if constexpr (C > 1) {
+        cg::this_cluster().barrier_wait();
+        if (rank != 0) return;
     }
-    // ---- the choice: a team of `threads` threads per row
-    const int threads = R >= 8 ? 32 : kSelThreads / R;
-    const int teams = kSelThreads / threads;
-    const int team = tid / threads, lt = tid % threads, team_warp0 = team * (threads / 32);
-    auto team_sum = [&](int32_t v, int &turn) {
-        v = __reduce_add_sync(0xffffffffu, v);
-        if (threads == 32) return v;
-        if (lane == 0) warp_count[turn][warp] = v;
-        team_sync(team, threads);
-        int32_t t = 0;
-        for (int w = 0; w < threads / 32; ++w) t += warp_count[turn][team_warp0 + w];
-        turn ^= 1;
-        return t;
+    // ---- the choice
+    auto row_of = [&](int r) {
+        SelRow x;
+        int first = r;                                         // its run's first row holds the means' norm
+        while (first > 0 && rows[first - 1].b == rows[r].b) --first;
+        x.sc = sc + (int64_t)r * a.ld;
+        x.q = sq + r * D;
+        x.P = means_of(rows[r].b);
+        x.ldp = ldp;
+        x.out = a.idx + ((int64_t)(row0 + r) * g.N2 + n) * g.count;
+        x.ns = segs[r];
+        x.init = g.init;
+        x.local = g.local;
+        x.count = g.count;
+        const float norm = __uint_as_float(pnorm[first]);
+        // (squares below 1e-30 have lost bits; products below 1e-38 are lost)
+        x.err = pbits[first] == 0 || qnorm[r] == 0.f ? 0.f
+                : norm < 1e-30f ? INFINITY : 8.f / 65536.f * qnorm[r] * sqrtf(norm) * 1.0001f + 1e-35f;
+        return x;
     };
-    int turn = 0;
-    for (int r = team; r < nr; r += teams) {
+    auto all_of = [&](int r, int t, int T) {                   // few segments: all are chosen
         int32_t *out = a.idx + ((int64_t)(row0 + r) * g.N2 + n) * g.count;
-        const int32_t ns = segs_of(rows[r]);
+        const int32_t ns = segs[r];
+        for (int32_t k = t; k < g.count; k += T) out[k] = k < ns ? k : -1;
+    };
+    for (int r = warp; r < nr; r += kSelThreads / 32) {
+        const int32_t ns = segs[r];
         if (ns <= g.count) {
-            for (int32_t k = lt; k < g.count; k += threads) out[k] = k < ns ? k : -1;
+            all_of(r, lane, 32);
             continue;
         }
-        const double *mine = sc + (int64_t)r * a.ld;
-        const int32_t lo_s = g.init, hi_s = ns - g.local;            // the free choice: [lo_s, hi_s)
-        const int32_t need = g.count - g.init - g.local;
-        // the largest threshold that at least `need` scores reach
-        uint64_t lo = 0, hi = ~0ull;
-        bool exact = need == 0;
-        while (lo < hi && !exact) {
-            const uint64_t mid = lo + ((hi - lo) >> 1) + ((hi - lo) & 1);
-            int32_t c = 0;
-            for (int32_t s = lo_s + lt; s < hi_s; s += threads) c += order_of(mine[s]) >= mid;
-            c = team_sum(c, turn);
-            if (c >= need) lo = mid;
-            else hi = mid - 1;
-            exact = c == need;
-        }
-        // `exact`: everything from lo on; else what lies above lo, and the
-        // first ones at lo itself
-        int32_t ties = 0;
-        if (!exact) {
-            int32_t c = 0;
-            for (int32_t s = lo_s + lt; s < hi_s; s += threads) c += order_of(mine[s]) > lo;
-            ties = need - team_sum(c, turn);
-        }
-        int32_t done = 0, tied = 0;
-        for (int32_t base = 0; base < ns; base += threads) {
-            const int32_t s = base + lt;
-            bool in = false, at = false;
-            if (s < ns) {
-                if (s < lo_s || s >= hi_s) in = true;
-                else if (need > 0) {
-                    const uint64_t u = order_of(mine[s]);
-                    in = exact ? u >= lo : u > lo;
-                    at = !exact && u == lo;
-                }
-            }
-            const uint32_t below = (1u << lane) - 1u;
-            if (!exact) {
-                // ranks among the ties, in order
-                uint32_t m = __ballot_sync(0xffffffffu, at);
-                int32_t rank = tied + __popc(m & below), sum = __popc(m);
-                if (threads > 32) {
-                    if (lane == 0) warp_count[turn][warp] = sum;
-                    team_sync(team, threads);
-                    sum = 0;
-                    for (int w = 0; w < threads / 32; ++w) {
-                        if (team_warp0 + w < warp) rank += warp_count[turn][team_warp0 + w];
-                        sum += warp_count[turn][team_warp0 + w];
-                    }
-                    turn ^= 1;
-                }
-                if (at && rank < ties) in = true;
-                tied += sum;
-            }
-            const uint32_t m = __ballot_sync(0xffffffffu, in);
-            int32_t rank = done + __popc(m & below), sum = __popc(m);
-            if (threads > 32) {
-                if (lane == 0) warp_count[turn][warp] = sum;
-                team_sync(team, threads);
-                sum = 0;
-                for (int w = 0; w < threads / 32; ++w) {
-                    if (team_warp0 + w < warp) rank += warp_count[turn][team_warp0 + w];
-                    sum += warp_count[turn][team_warp0 + w];
-                }
-                turn ^= 1;
-            }
-            if (in) out[rank] = s;
-            done += sum;
-        }
+        if (ns > 1024) continue;
+        const SelRow x = row_of(r);
+        const bool ok = ns <= 256 ? choose<D, 8, false>(x, sh, warp)
+                        : ns <= 512 ? choose<D, 16, false>(x, sh, warp) : choose<D, 32, false>(x, sh, warp);
+        if (!ok && lane == 0) unsettled[atomicAdd(&unsettled_n, 1)] = r;
     }
+    __syncthreads();
+    if (most <= g.count) return;
+    // rows of more segments than a warp's registers hold: the block
+    for (int r = 0; r < nr; ++r) {
+        if (segs[r] <= 1024 || segs[r] <= g.count) continue;
+        const bool ok = choose<D, 0, true>(row_of(r), sh, 0);
+        if (!ok && tid == 0) unsettled[unsettled_n++] = r;
+        __syncthreads();
+    }
+    // (the order of these rows does not matter; the scores of the others are no longer needed)
+    for (int k = 0; k < unsettled_n; ++k) choose_exactly<D>(row_of(unsettled[k]), sh, reinterpret_cast<double *>(sc));
 }
 
 bool off(const void *p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; }
 
-template <int D, bool F16>
-cudaError_t launch_select(SelArgs a, int R, size_t smem, cudaStream_t s)
+template <int D, bool F16, int MT, int C>
+cudaError_t launch_select(const SelArgs &a, size_t smem, cudaStream_t s)
 {
-    auto kern = select_kernel<D, F16>;
+    auto kern = select_kernel<D, F16, MT, C>;
     const cudaError_t e = li::set_max_dynamic_smem(reinterpret_cast<const void *>(kern), (int)smem);
     if (e != cudaSuccess) return e;
-    a.R = R;
-    kern<<<dim3((unsigned)((a.g.rows + R - 1) / R), (unsigned)a.g.N2), kSelThreads, smem, s>>>(a);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((a.g.rows + a.R - 1) / a.R) * C, (unsigned)a.g.N2);
+    cfg.blockDim = dim3(kSelThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = C;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = C > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, a);
+}
+
+template <int D, bool F16>
+cudaError_t launch_select(const SelArgs &a, int split, size_t smem, cudaStream_t s)
+{
+    if (split == 8) return launch_select<D, F16, 1, 8>(a, smem, s);
+    if (split == 4) return launch_select<D, F16, 1, 4>(a, smem, s);
+    if (split == 2) return launch_select<D, F16, 1, 2>(a, smem, s);
+    return a.R > 16 ? launch_select<D, F16, 2, 1>(a, smem, s) : launch_select<D, F16, 1, 1>(a, smem, s);
 }
 
 }  // namespace
@@ -501,21 +862,27 @@ extern "C" LI_API li_status li_segment_select(const li_segment_params *p, const 
     a.q = static_cast<const uint16_t *>(query);
     a.pooled = pooled;
     a.idx = seg_idx;
-    // rows per block: a power of two, with the scores within 100 KB (two blocks
-    // per SM) while more than one row fits, and not so many that SMs stay idle
+    // rows per block: as many as stand within 110 KB (two blocks per SM), and not
+    // so many that SMs stay idle
     const int sms = seg_sms(), D = p->D;
-    a.ld = (p->max_segs + 1) & ~1;
-    auto bytes = [&](int R) {
-        const size_t parts = (size_t)kSelThreads * 8 * 8, scores = (size_t)R * a.ld * 8;
-        return (size_t)((R + 7) & ~7) * (D + 2) * 8 + (scores > parts ? scores : parts);
+    a.ld = ((p->max_segs + 31) & ~31) + 8;               // rows of a fragment fall into different banks
+    auto bytes = [&](int R, bool split) {
+        const size_t sums = (size_t)kSelThreads * 8 * 8, scores = (size_t)(R > 2 ? R : 2) * a.ld * 4;
+        return (size_t)R * D * 8 + (size_t)(R > 16 ? 2 : 1) * D * 64 + (split ? scores + sums : scores > sums ? scores : sums);
     };
     int R = kSelRows;
-    while (R > 1 && (bytes(R) > 100 * 1024 || (int64_t)((a.g.rows + R - 1) / R) * p->N2 < 2 * sms)) R /= 2;
-    const size_t smem = bytes(R);
+    while (R > 1 && bytes(R, false) > 110 * 1024) --R;
+    while (R > 1 && (int64_t)((a.g.rows + R - 1) / R) * p->N2 < 2 * sms) R = (R + 1) / 2;
+    // few rows: a cluster shares a row's segments, at least 128 to a block
+    int split = 1;
+    if (R == 1)
+        while (split < kSelSplit && (int64_t)a.g.rows * p->N2 * split * 2 <= 2LL * sms && p->max_segs >= 2 * split * 128) split *= 2;
+    a.R = R;
+    const size_t smem = bytes(R, split > 1);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool f16 = p->dtype == LI_FP16;
-    const cudaError_t e = D == 128 ? (f16 ? launch_select<128, true>(a, R, smem, s) : launch_select<128, false>(a, R, smem, s))
-                                   : (f16 ? launch_select<64, true>(a, R, smem, s) : launch_select<64, false>(a, R, smem, s));
+    const cudaError_t e = D == 128 ? (f16 ? launch_select<128, true>(a, split, smem, s) : launch_select<128, false>(a, split, smem, s))
+                                   : (f16 ? launch_select<64, true>(a, split, smem, s) : launch_select<64, false>(a, split, smem, s));
     if (e != cudaSuccess) return seg_fail(call, LI_ERR_CUDA, cudaGetErrorString(e));
     li::set_launch_count(1);
     return LI_OK;
