@@ -5,6 +5,7 @@
 #include <cmath>
 #include <cstdio>
 
+#include "attn_common.cuh"
 #include "li_segment.cuh"
 
 namespace li {
@@ -240,33 +241,41 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t 
     lo = *reinterpret_cast<const uint32_t *>(&l);
 }
 
-// Order of the scores as unsigned integers (-0 = +0; in 64 bits NaN lowest).
+// Order of 64-bit scores as unsigned integers (NaN lowest, -0 = +0).
 __device__ __forceinline__ uint64_t order_of(double x)
 {
     if (x != x) return 0;
     const uint64_t u = (uint64_t)__double_as_longlong(x + 0.0);
     return u >> 63 ? ~u : u | 0x8000000000000000ull;
 }
-__device__ __forceinline__ uint32_t order_of(float x)      // NaN above inf; 0 is not used
-{
-    uint32_t u = __float_as_uint(x);
-    u = u == 0x80000000u ? 0u : u;
-    return (u & 0x7FFFFFFFu) > 0x7F800000u ? 0xFFFFFFFFu : u >> 31 ? ~u : u | 0x80000000u;
-}
-__device__ __forceinline__ float value_of(uint32_t u) { return __uint_as_float(u >> 31 ? u & 0x7FFFFFFFu : ~u); }
 
-// q . P[s] in 64 bits, by a warp.
-template <int D>
+__device__ __forceinline__ float warp_min(float x)
+{
+    float m;
+    asm volatile("redux.sync.min.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(x));
+    return m;
+}
+__device__ __forceinline__ float warp_max(float x)
+{
+    float m;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(x));
+    return m;
+}
+
+// q . P[s] in 64 bits, by 32 or 8 neighbouring lanes (T).
+template <int D, int T>
 __device__ __forceinline__ double exact_score(const double *q, const float *P, int64_t ldp, int32_t s, int lane)
 {
     double x = 0;
-    if (lane < D / 4) {
-        const float4 p = reinterpret_cast<const float4 *>(P + s * ldp)[lane];
-        const double2 a = reinterpret_cast<const double2 *>(q)[2 * lane], b = reinterpret_cast<const double2 *>(q)[2 * lane + 1];
-        x = a.x * p.x + a.y * p.y + b.x * p.z + b.y * p.w;
+    const float4 *p = reinterpret_cast<const float4 *>(P + s * ldp);
+#pragma unroll
+    for (int c = lane % T; c < D / 4; c += T) {
+        const float4 v = p[c];
+        const double2 a = reinterpret_cast<const double2 *>(q)[2 * c], b = reinterpret_cast<const double2 *>(q)[2 * c + 1];
+        x += (a.x * v.x + a.y * v.y) + (b.x * v.z + b.y * v.w);
     }
 #pragma unroll
-    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    for (int o = T / 2; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     return x;
 }
 
@@ -283,7 +292,7 @@ struct SelRow {
 
 struct SelShared {
     int32_t sums[2][kSelThreads / 32];
-    uint32_t lows[kSelThreads / 32], highs[kSelThreads / 32];
+    float lows[kSelThreads / 32], highs[kSelThreads / 32];
     int32_t band[kSelThreads / 32][32];    // segments near the border, per team
     int32_t bands[kSelThreads / 32];
     uint32_t taken[kSelThreads / 32];
@@ -313,105 +322,152 @@ __device__ bool choose(const SelRow &r, SelShared &sh, int team)
         }
         return v;
     };
-    auto least = [&](uint32_t lo) {
-        lo = __reduce_min_sync(0xffffffffu, lo);
+    auto least = [&](float lo) {
+        lo = warp_min(lo);
         if constexpr (WIDE) {
             __syncthreads();
             if (lane == 0) sh.lows[warp] = lo;
             __syncthreads();
-            for (int w = 0; w < kSelThreads / 32; ++w) lo = sh.lows[w] < lo ? sh.lows[w] : lo;
+            for (int w = 0; w < kSelThreads / 32; ++w) lo = fminf(lo, sh.lows[w]);
         }
         return lo;
     };
-    auto most = [&](uint32_t hi) {
-        hi = __reduce_max_sync(0xffffffffu, hi);
+    auto most = [&](float hi) {
+        hi = warp_max(hi);
         if constexpr (WIDE) {
             __syncthreads();
             if (lane == 0) sh.highs[warp] = hi;
             __syncthreads();
-            for (int w = 0; w < kSelThreads / 32; ++w) hi = sh.highs[w] > hi ? sh.highs[w] : hi;
+            for (int w = 0; w < kSelThreads / 32; ++w) hi = fmaxf(hi, sh.highs[w]);
         }
         return hi;
     };
-    // scores as ordered integers; 0: not of the free choice [from, to)
+    // the free choice is from [from, to); others read as -inf
     const int32_t from = r.init, to = r.ns - r.local, need = r.count - r.init - r.local;
-    auto key_at = [&](int32_t s) -> uint32_t { return s >= from && s < to ? order_of(r.sc[s]) : 0u; };
-    uint32_t key[KR > 0 ? KR : 1];
+    auto score_at = [&](int32_t s) { return s >= from && s < to ? r.sc[s] : -INFINITY; };
+    float held[KR > 0 ? KR : 1];                       // a lane's KR neighbouring segments
+    // (conditions on them are written with & and as bit masks: a branch for each
+    // would cost more than all the rest)
+    auto bits_of = [&](int32_t lo, int32_t hi) {       // those within [lo, hi)
+        lo -= t * KR;
+        hi -= t * KR;
+        lo = lo < 0 ? 0 : (lo > KR ? KR : lo);
+        hi = hi < 0 ? 0 : (hi > KR ? KR : hi);
+        return (uint32_t)((1ull << hi) - 1) & ~(uint32_t)((1ull << lo) - 1);
+    };
+    const uint32_t free_bits = KR > 0 ? bits_of(from, to) : 0;
     if constexpr (KR > 0) {
 #pragma unroll
-        for (int k = 0; k < KR; ++k) key[k] = key_at(k * T + t);
+        for (int k = 0; k < KR; k += 4) {
+            const int32_t s = t * KR + k;
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (s < r.ns) x = *reinterpret_cast<const float4 *>(r.sc + s);
+            held[k] = free_bits >> k & 1u ? x.x : -INFINITY;
+            held[k + 1] = free_bits >> (k + 1) & 1u ? x.y : -INFINITY;
+            held[k + 2] = free_bits >> (k + 2) & 1u ? x.z : -INFINITY;
+            held[k + 3] = free_bits >> (k + 3) & 1u ? x.w : -INFINITY;
+        }
     }
-    auto each = [&](auto &&f) {                        // f(segment, key), all of the row's segments
+    auto each = [&](auto &&f) {                        // f(segment, score), all of the row's segments
         if constexpr (KR > 0) {
 #pragma unroll
-            for (int k = 0; k < KR; ++k) f(k * T + t, key[k]);
+            for (int k = 0; k < KR; ++k) f(t * KR + k, held[k]);
         } else {
-            for (int32_t s = t; s < r.ns; s += T) f(s, key_at(s));
+            for (int32_t s = t; s < r.ns; s += T) f(s, score_at(s));
         }
     };
-    // chosen: keys from `cut` on; with a band also the ones of it that are `taken`
-    uint32_t cut = 1, band_lo = 1, band_hi = 0, taken = 0;
+    // chosen: scores from `cut` on and above `over`; of those within [band_lo,
+    // band_hi] the ones that are `taken`
+    float cut = INFINITY, over = -INFINITY, band_lo = INFINITY, band_hi = -INFINITY;
+    uint32_t taken = 0;
     int32_t ties = 0;                                  // equal scores of the cut that are chosen, lowest first (0: all)
     if (need > 0) {
-        uint32_t lo = 0xffffffffu, hi = 0;
-        each([&](int32_t, uint32_t k) {
-            lo = k && k < lo ? k : lo;
-            hi = k > hi ? k : hi;
-        });
+        float lo = INFINITY, hi = -INFINITY;
+        bool odd = false;
+        if constexpr (KR > 0) {
+#pragma unroll
+            for (int k = 0; k < KR; ++k) {
+                const bool is = free_bits >> k & 1u;
+                odd |= is & !(fabsf(held[k]) < 1e38f);
+                lo = fminf(lo, is ? held[k] : INFINITY);
+                hi = fmaxf(hi, held[k]);
+            }
+        } else {
+            for (int32_t s = from + t; s < to; s += T) {
+                const float x = r.sc[s];
+                odd |= !(fabsf(x) < 1e38f);
+                lo = fminf(lo, x);
+                hi = fmaxf(hi, x);
+            }
+        }
+        odd = sum(odd) > 0;
+        if (odd || !(r.err < INFINITY)) return false;
         lo = least(lo);
         hi = most(hi);
-        // not finite: the ordered integers of -inf, +inf and NaN lie outside
-        if (lo <= order_of(-INFINITY) || hi >= order_of(INFINITY) || !(r.err < INFINITY)) return false;
+        // at least `need` scores from lo on, fewer from hi on
+        hi = hi == 0.f ? 1e-45f : __int_as_float(__float_as_int(hi) + (hi > 0.f ? 1 : -1));
         bool even = false;                             // exactly `need` scores from lo on
-        while (lo < hi && !even) {
-            const uint32_t mid = lo + ((hi - lo) >> 1) + ((hi - lo) & 1);
+        for (;;) {
+            const float mid = 0.5f * lo + 0.5f * hi;
+            if (!(mid > lo && mid < hi)) break;
             int32_t c = 0;
-            each([&](int32_t, uint32_t k) { c += k >= mid; });
+            if constexpr (KR > 0) {                    // four sums: adds that do not wait for one another
+                int32_t c4[4] = {};
+#pragma unroll
+                for (int k = 0; k < KR; ++k) c4[k & 3] += held[k] >= mid;
+                c = (c4[0] + c4[1]) + (c4[2] + c4[3]);
+            } else {
+                each([&](int32_t, float x) { c += x >= mid; });
+            }
             c = sum(c);
             if (c >= need) lo = mid;
-            else hi = mid - 1;
-            even = c == need;
+            else hi = mid;
+            if (c == need) {
+                even = true;
+                break;
+            }
         }
-        cut = lo;
+        // the last score chosen, and the first one left out
+        float in = INFINITY, out = -INFINITY;
+        each([&](int32_t, float x) {
+            in = fminf(in, x >= lo ? x : INFINITY);
+            out = fmaxf(out, x >= lo ? -INFINITY : x);
+        });
+        cut = least(in);
         if (even) {
-            uint32_t in = 0xffffffffu, out = 0;
-            each([&](int32_t, uint32_t k) {
-                if (k >= cut) in = k < in ? k : in;
-                else out = k > out ? k : out;
-            });
-            cut = least(in);
             out = most(out);
-            even = out == 0 || value_of(cut) - value_of(out) > 2.f * r.err;
+            even = cut - out > 2.f * r.err;
         }
         if (!even) {
             if (r.err == 0.f) {                        // every score is exact (zero): only ties
                 int32_t c = 0;
-                each([&](int32_t, uint32_t k) { c += k > cut; });
+                each([&](int32_t, float x) { c += x > cut; });
                 ties = need - sum(c);
             } else {
-                const float v = value_of(cut);
-                band_lo = order_of(v - 2.f * r.err);
-                band_hi = order_of(v + 2.f * r.err);
+                band_lo = cut - 2.f * r.err;
+                band_hi = cut + 2.f * r.err;
                 int32_t above = 0, inside = 0;
-                each([&](int32_t, uint32_t k) {
-                    above += k > band_hi;
-                    inside += k >= band_lo && k <= band_hi;
+                each([&](int32_t, float x) {
+                    above += x > band_hi;
+                    inside += (x >= band_lo) & (x <= band_hi);
                 });
                 above = sum(above);
                 inside = sum(inside);
                 if (inside > 32) return false;
                 if (t == 0) sh.bands[team] = 0;
                 sync();
-                each([&](int32_t s, uint32_t k) {
-                    if (k >= band_lo && k <= band_hi) sh.band[team][atomicAdd(&sh.bands[team], 1)] = s;
+                each([&](int32_t s, float x) {
+                    if ((x >= band_lo) & (x <= band_hi)) sh.band[team][atomicAdd(&sh.bands[team], 1)] = s;
                 });
                 sync();
                 if (!WIDE || warp == 0) {              // one warp ranks them: score, then the lower segment
                     double mine = 0;
                     const int32_t s = lane < inside ? sh.band[team][lane] : 0;
-                    for (int i = 0; i < inside; ++i) {
-                        const double x = exact_score<D>(r.q, r.P, r.ldp, sh.band[team][i], lane);
-                        if (lane == i) mine = x;
+                    for (int i = 0; i < inside; i += 4) {
+                        const int k = i + (lane >> 3);
+                        const double x = exact_score<D, 8>(r.q, r.P, r.ldp, sh.band[team][k < inside ? k : inside - 1], lane);
+                        const double y = __shfl_sync(0xffffffffu, x, (lane - i) * 8 & 31);
+                        if (lane >= i && lane < i + 4) mine = y;
                     }
                     const uint64_t ord = order_of(mine);
                     int rank = 0;
@@ -425,13 +481,43 @@ __device__ bool choose(const SelRow &r, SelShared &sh, int team)
                 }
                 sync();
                 taken = sh.taken[team];
-                cut = band_hi + 1;
+                over = band_hi;
             }
         }
     }
     // in order: the forced ones, and the chosen
     const uint32_t below = (1u << lane) - 1u;
     int32_t done = 0, tied = 0;
+    if constexpr (KR > 0) {
+        uint32_t mine = bits_of(0, r.ns) & ~free_bits; // bit k: segment t * KR + k
+#pragma unroll
+        for (int k = 0; k < KR; ++k) mine |= (held[k] >= cut) & (held[k] > over) ? 1u << k : 0u;
+        for (uint32_t m = taken; m; m &= m - 1) {
+            const int32_t s = sh.band[team][__ffs(m) - 1];
+            if (s / KR == t) mine |= 1u << (s % KR);
+        }
+        auto before = [&](int32_t v) {                 // sum over the lanes below
+            const int32_t own = v;
+#pragma unroll
+            for (int o = 1; o < 32; o *= 2) {
+                const int32_t u = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v += u;
+            }
+            return v - own;
+        };
+        if (ties > 0) {
+            int32_t c = 0;
+#pragma unroll
+            for (int k = 0; k < KR; ++k) c += held[k] == cut;
+            int32_t rank = before(c);
+#pragma unroll
+            for (int k = 0; k < KR; ++k)
+                if (held[k] == cut && rank++ >= ties) mine &= ~(1u << k);
+        }
+        int32_t *out = r.out + before(__popc(mine));
+        for (; mine; mine &= mine - 1) *out++ = t * KR + __ffs(mine) - 1;
+        return true;
+    }
     auto place = [&](bool b, int32_t base, int32_t &total) {   // rank of this thread's among the team's in order
         const uint32_t m = __ballot_sync(0xffffffffu, b);
         int32_t rank = base + __popc(m & below);
@@ -448,27 +534,21 @@ __device__ bool choose(const SelRow &r, SelShared &sh, int team)
         }
         return rank;
     };
-    auto step = [&](int32_t s, uint32_t k) {
-        bool in = s < r.ns && (k == 0 || (need > 0 && k >= cut));
-        if (k >= band_lo && k <= band_hi) {
-            in = false;
+    for (int32_t s0 = 0; s0 < r.ns; s0 += T) {
+        const int32_t s = s0 + t;
+        const float x = s < r.ns ? score_at(s) : -INFINITY;
+        bool in = s < r.ns && (s < from || s >= to || (x >= cut && x > over));
+        if (x >= band_lo && x <= band_hi)
             for (uint32_t m = taken; m; m &= m - 1) in |= sh.band[team][__ffs(m) - 1] == s;
-        }
         int32_t total;
         if (ties > 0) {
-            const int32_t rank = place(k == cut, tied, total);
-            if (k == cut && rank >= ties) in = false;
+            const int32_t rank = place(x == cut, tied, total);
+            if (x == cut && rank >= ties) in = false;
             tied += total;
         }
         const int32_t rank = place(in, done, total);
         if (in) r.out[rank] = s;
         done += total;
-    };
-    if constexpr (KR > 0) {
-#pragma unroll
-        for (int k = 0; k < KR; ++k) step(k * T + t, key[k]);
-    } else {
-        for (int32_t s0 = 0; s0 < r.ns; s0 += T) step(s0 + t, s0 + t < r.ns ? key_at(s0 + t) : 0u);
     }
     return true;
 }
@@ -481,7 +561,7 @@ __device__ void choose_exactly(const SelRow &r, SelShared &sh, double *x)
     const int32_t from = r.init, to = r.ns - r.local, need = r.count - r.init - r.local;
     __syncthreads();
     for (int32_t s = warp; s < r.ns; s += kSelThreads / 32) {
-        const double v = exact_score<D>(r.q, r.P, r.ldp, s, lane);
+        const double v = exact_score<D, 32>(r.q, r.P, r.ldp, s, lane);
         if (lane == 0) x[s] = v;
     }
     __syncthreads();
@@ -539,13 +619,14 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelArgs a)
     const SegGeo &g = a.g;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int R = a.R;
-    double *sq = dyn;                                          // [R][D]
-    uint4 *frag = reinterpret_cast<uint4 *>(sq + R * D);       // [MT][KS][2][32]: q's two parts as fragments
+    double *sq = dyn;                                          // [R][D + 2]: rows of a fragment fall into different banks
+    uint4 *frag = reinterpret_cast<uint4 *>(sq + R * (D + 2));       // [MT][KS][2][32]: q's two parts as fragments
     float *sc = reinterpret_cast<float *>(frag + MT * KS * 64);                   // [R][ld]
     double *red = reinterpret_cast<double *>(sc + (C > 1 ? (size_t)(R > 2 ? R : 2) * a.ld : 0));   // partial sums of q
     __shared__ SegRow rows[kSelRows];
     __shared__ int32_t segs[kSelRows], most_segs;
     __shared__ float qnorm[kSelRows];
+    __shared__ int32_t leader[kSelRows];                       // the first row of a row's run (of rows of one batch)
     __shared__ uint32_t pnorm[kSelRows], pbits[kSelRows];      // of a run's means: largest |P|^2, all bits; at its first row
     __shared__ int32_t unsettled[kSelRows], unsettled_n;
     __shared__ SelShared sh;
@@ -570,6 +651,9 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelArgs a)
             segs[lane] = ns;
             pnorm[lane] = pbits[lane] = 0;
         }
+        const int32_t left = __shfl_up_sync(0xffffffffu, r.b, 1);
+        const uint32_t starts = __ballot_sync(0xffffffffu, lane == 0 || left != r.b);
+        if (lane < R) leader[lane] = 31 - __clz(starts & (0xffffffffu >> (31 - lane)));
         ns = __reduce_max_sync(0xffffffffu, ns);
         if (lane == 0) {
             most_segs = ns;
@@ -591,7 +675,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelArgs a)
             double acc[8] = {};
             if (e < per && part < parts && r < nr && rows[r].vis > 0) {
                 const uint16_t *src = a.q + ((int64_t)(row0 + r) * g.N1 + (int64_t)n * g.G) * D + c;
-#pragma unroll 4
+#pragma unroll 16
                 for (int h = part; h < g.G; h += parts) {
                     const uint4 v = *reinterpret_cast<const uint4 *>(src + (int64_t)h * D);
                     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -603,7 +687,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelArgs a)
                 }
             }
             if (e < per && part < parts) {
-                double *dst = parts > 1 ? red + ((int64_t)part * R + r) * D + c : sq + r * D + c;
+                double *dst = parts > 1 ? red + ((int64_t)part * R + r) * D + c : sq + r * (D + 2) + c;
 #pragma unroll
                 for (int k = 0; k < 8; ++k) dst[k] = acc[k];
             }
@@ -613,7 +697,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelArgs a)
             for (int e = tid; e < R * D; e += kSelThreads) {
                 double acc = 0;
                 for (int k = 0; k < parts; ++k) acc += red[k * R * D + e];
-                sq[e] = acc;
+                sq[e / D * (D + 2) + e % D] = acc;
             }
             __syncthreads();
         }
@@ -625,7 +709,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelArgs a)
 #pragma unroll
             for (int h = 0; h < 4; ++h) {
                 const int r = mt * 16 + (l >> 2) + (h & 1) * 8, c = ks * 16 + 4 * (l & 3) + (h >> 1) * 2;
-                const double x = r < R ? sq[r * D + c] : 0, y = r < R ? sq[r * D + c + 1] : 0;
+                const double x = r < R ? sq[r * (D + 2) + c] : 0, y = r < R ? sq[r * (D + 2) + c + 1] : 0;
                 split2((float)x, (float)y, hi[h], lo[h]);
             }
             uint4 *dst = frag + (mt * KS + ks) * 64 + l;
@@ -634,7 +718,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelArgs a)
         }
         for (int r = warp; r < R; r += kSelThreads / 32) {
             double x = 0;
-            for (int c = lane; c < D; c += 32) x = fma(sq[r * D + c], sq[r * D + c], x);
+            for (int c = lane; c < D; c += 32) x = fma(sq[r * (D + 2) + c], sq[r * (D + 2) + c], x);
 #pragma unroll
             for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
             if (lane == 0) qnorm[r] = x > 0 ? fmaxf((float)sqrt(x) * 1.0001f, 1e-30f) : (x == 0 ? 0.f : INFINITY);
@@ -689,13 +773,15 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelArgs a)
                 }
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
-                    float x = 0.f;
+                    float x = 0.f, y = 0.f;
 #pragma unroll
                     for (int k = 0; k < KS; ++k) {
                         const float4 v = p[t][k];
-                        x = fmaf(v.x, v.x, fmaf(v.y, v.y, fmaf(v.z, v.z, fmaf(v.w, v.w, x))));
+                        ffma2(x, y, v.x, v.y, v.x, v.y, x, y);
+                        ffma2(x, y, v.z, v.w, v.z, v.w, x, y);
                         bits |= __float_as_uint(v.x) | __float_as_uint(v.y) | __float_as_uint(v.z) | __float_as_uint(v.w);
                     }
+                    x += y;
                     x += __shfl_xor_sync(0xffffffffu, x, 1);
                     x += __shfl_xor_sync(0xffffffffu, x, 2);
                     norm = fmaxf(norm, x);
@@ -738,10 +824,9 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelArgs a)
     // ---- the choice
     auto row_of = [&](int r) {
         SelRow x;
-        int first = r;                                         // its run's first row holds the means' norm
-        while (first > 0 && rows[first - 1].b == rows[r].b) --first;
+        const int first = leader[r];                           // holds the norm of the run's means
         x.sc = sc + (int64_t)r * a.ld;
-        x.q = sq + r * D;
+        x.q = sq + r * (D + 2);
         x.P = means_of(rows[r].b);
         x.ldp = ldp;
         x.out = a.idx + ((int64_t)(row0 + r) * g.N2 + n) * g.count;
@@ -868,11 +953,16 @@ extern "C" LI_API li_status li_segment_select(const li_segment_params *p, const 
     a.ld = ((p->max_segs + 31) & ~31) + 8;               // rows of a fragment fall into different banks
     auto bytes = [&](int R, bool split) {
         const size_t sums = (size_t)kSelThreads * 8 * 8, scores = (size_t)(R > 2 ? R : 2) * a.ld * 4;
-        return (size_t)R * D * 8 + (size_t)(R > 16 ? 2 : 1) * D * 64 + (split ? scores + sums : scores > sums ? scores : sums);
+        return (size_t)R * (D + 2) * 8 + (size_t)(R > 16 ? 2 : 1) * D * 64 + (split ? scores + sums : scores > sums ? scores : sums);
     };
     int R = kSelRows;
     while (R > 1 && bytes(R, false) > 110 * 1024) --R;
     while (R > 1 && (int64_t)((a.g.rows + R - 1) / R) * p->N2 < 2 * sms) R = (R + 1) / 2;
+    // the fewest rows that take as many waves (8192 rows, 4 key heads, 512 segments:
+    // 28 rows, not 31, fill the last of 4)
+    const int64_t blocks = (int64_t)((a.g.rows + R - 1) / R) * p->N2, waves = (blocks + 2 * sms - 1) / (2 * sms);
+    const int64_t per_head = waves * 2 * sms / p->N2;
+    if (per_head > 0 && (a.g.rows + per_head - 1) / per_head < R) R = (int)((a.g.rows + per_head - 1) / per_head);
     // few rows: a cluster shares a row's segments, at least 128 to a block
     int split = 1;
     if (R == 1)
