@@ -11,8 +11,10 @@
 // blocks are resident when the plan ends.
 //
 // Bounds: the tables are a few hundred kilobytes, so small calls are bound by
-// the latency of two dependent launches and one scan; copies are bound by HBM
-// (each page read once and written once).
+// the latency of two dependent launches and one scan (5 to 7 us; one launch of a
+// cluster with a barrier between the steps took 8.6 us for a reservation where
+// these take 6.6); copies are bound by HBM (each page read once and written
+// once, in accesses marked as used once).
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -37,6 +39,7 @@ constexpr int kPassPages = kPlanThreads * 4 * kQuads;     // 32768 pages
 constexpr int kApplyThreads = 256;
 constexpr int kChunk = 16384;                             // bytes a block copies at a time
 constexpr int kMaxPools = 64;                             // descriptors of one launch
+constexpr int kFewPools = 4;                              // of a launch with short parameters
 constexpr int kMaxPoolsCall = 256;
 
 enum Op { kReserve, kFork, kFree, kCompact };
@@ -63,9 +66,10 @@ struct PagesArgs {
     int32_t P, ps, cols, B, n;
 };
 
+template <int N>
 struct Pools {
-    char *base[kMaxPools];
-    int64_t bytes[kMaxPools], stride[kMaxPools];
+    char *base[N];
+    int64_t bytes[N], stride[N];
     int32_t n;
 };
 
@@ -257,12 +261,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PagesArgs a)
         int32_t need = 0;
         if (i < n) {
             if (OP == kReserve) {
-                const int32_t len = a.old[i], want = a.arg0[i];
+                const int32_t len = clamp_len(a, a.lens[i]), want = a.arg0[i];
                 if (want < 0 || want > a.cols * a.ps) flag(a.status, LI_DEV_BAD_KLEN);
                 need = growth(a, len, want);
             } else {
                 const int32_t r = a.arg1[i];
-                if (r >= 0 && r < a.B && a.claim[r] == i) need = a.old[a.arg0[i]] % a.ps != 0;
+                if (r >= 0 && r < a.B && a.claim[r] == i) need = clamp_len(a, a.lens[a.arg0[i]]) % a.ps != 0;
                 else if (r >= 0 && r < a.B && a.claim[r] != 0x7FFFFFFF) flag(a.status, LI_DEV_BAD_ROW);
             }
         }
@@ -305,19 +309,20 @@ __device__ __forceinline__ void copy_run(char *dst, const char *src, int64_t byt
     const int n = (int)(bytes / (int64_t)sizeof(V));
     int i = threadIdx.x;
     for (; i + 3 * kApplyThreads < n; i += 4 * kApplyThreads) {
-        const V x0 = s[i], x1 = s[i + kApplyThreads], x2 = s[i + 2 * kApplyThreads], x3 = s[i + 3 * kApplyThreads];
-        d[i] = x0;
-        d[i + kApplyThreads] = x1;
-        d[i + 2 * kApplyThreads] = x2;
-        d[i + 3 * kApplyThreads] = x3;
+        const V x0 = __ldcs(s + i), x1 = __ldcs(s + i + kApplyThreads), x2 = __ldcs(s + i + 2 * kApplyThreads),
+                x3 = __ldcs(s + i + 3 * kApplyThreads);
+        __stcs(d + i, x0);
+        __stcs(d + i + kApplyThreads, x1);
+        __stcs(d + i + 2 * kApplyThreads, x2);
+        __stcs(d + i + 3 * kApplyThreads, x3);
     }
-    for (; i < n; i += kApplyThreads) d[i] = s[i];
+    for (; i < n; i += kApplyThreads) __stcs(d + i, __ldcs(s + i));
 }
 
 // Page contents: item = (pair, pool, chunk), dealt to the blocks in turn;
 // pair(i, src, dst) names the pages, or says that there is nothing to copy.
-template <typename Pair>
-__device__ void copy_pages(const Pools &pools, int32_t pairs, Pair pair)
+template <int N, typename Pair>
+__device__ void copy_pages(const Pools<N> &pools, int32_t pairs, Pair pair)
 {
     // chunks of one pair, over all pools
     int64_t per_pair = 0;
@@ -347,16 +352,16 @@ __device__ void copy_pages(const Pools &pools, int32_t pairs, Pair pair)
 
 // TABLES: write the new table, lengths and counts (the first launch of a call
 // does; further ones only copy the pools that did not fit into it).
-template <int OP, bool TABLES>
-__global__ void __launch_bounds__(kApplyThreads) apply_kernel(const PagesArgs a, const Pools pools)
+template <int OP, bool TABLES, int N>
+__global__ void __launch_bounds__(kApplyThreads) apply_kernel(const PagesArgs a, const __grid_constant__ Pools<N> pools)
 {
     grid_dependency_wait();
     const int64_t t0 = (int64_t)blockIdx.x * kApplyThreads + threadIdx.x, step = (int64_t)gridDim.x * kApplyThreads;
     const bool same_table = a.table == a.table_out;
     if (TABLES) {
-        const int64_t entries = (int64_t)a.B * a.cols;
-        for (int64_t e = t0; e < entries; e += step) {
-            const int32_t r = (int32_t)(e / a.cols), c = (int32_t)(e - (int64_t)r * a.cols);
+        const uint32_t entries = (uint32_t)(a.B * a.cols);       // < 2^31
+        for (uint32_t e = (uint32_t)t0; e < entries; e += (uint32_t)step) {
+            const int32_t r = (int32_t)(e / (uint32_t)a.cols), c = (int32_t)(e - (uint32_t)r * (uint32_t)a.cols);
             const int32_t len = a.old[r];
             int32_t new_len = len;
             bool write = !same_table;
@@ -465,7 +470,8 @@ __global__ void __launch_bounds__(kApplyThreads) apply_kernel(const PagesArgs a,
 
 // Pages by explicit number.
 __global__ void __launch_bounds__(kApplyThreads) copy_kernel(const int32_t *src_pages, const int32_t *dst_pages,
-                                                             int32_t n, int32_t P, int32_t *status, const Pools pools)
+                                                             int32_t n, int32_t P, int32_t *status,
+                                                             const __grid_constant__ Pools<kMaxPools> pools)
 {
     copy_pages(pools, n, [&](int32_t i, int32_t &src, int32_t &dst) {
         src = src_pages[i];
@@ -531,10 +537,11 @@ li_status check_pools(const char *call, const li_page_pool *pools, int32_t n)
     return LI_OK;
 }
 
-Pools some_pools(const li_page_pool *pools, int32_t from, int32_t n, int64_t *chunks)
+template <int N>
+Pools<N> some_pools(const li_page_pool *pools, int32_t from, int32_t n, int64_t *chunks)
 {
-    Pools out{};
-    out.n = n - from < kMaxPools ? n - from : kMaxPools;
+    Pools<N> out{};
+    out.n = n - from < N ? n - from : N;
     *chunks = 0;
     for (int k = 0; k < out.n; ++k) {
         out.base[k] = static_cast<char *>(pools[from + k].base);
@@ -552,21 +559,13 @@ int sm_count()
     return sms;
 }
 
-template <int OP>
-cudaError_t launch(const PagesArgs &a, const li_page_pool *pools, int32_t n_pools, cudaStream_t s, int *launches)
+template <int OP, int N>
+cudaError_t launch_apply(const PagesArgs &a, const li_page_pool *pools, int32_t n_pools, int sms, cudaStream_t s, int *launches)
 {
-    const int sms = sm_count();
-    int copy_blocks = 0;
-    if (OP != kCompact && a.refs != a.refs_out) {
-        copy_blocks = (a.P + kPlanThreads - 1) / kPlanThreads;
-        if (copy_blocks > sms - 1) copy_blocks = sms - 1;
-    }
-    plan_kernel<OP><<<1 + copy_blocks, kPlanThreads, 0, s>>>(a);
-    cudaError_t e = cudaGetLastError();
-    *launches = 1;
-    for (int32_t from = 0; e == cudaSuccess && (from == 0 || from < n_pools); from += kMaxPools) {
+    cudaError_t e = cudaSuccess;
+    for (int32_t from = 0; e == cudaSuccess && (from == 0 || from < n_pools); from += N) {
         int64_t chunks;
-        const Pools some = some_pools(pools, from, n_pools, &chunks);
+        const Pools<N> some = some_pools<N>(pools, from, n_pools, &chunks);
         int64_t blocks = from == 0 ? ((int64_t)a.B * a.cols + kApplyThreads - 1) / kApplyThreads : 1;
         if (OP == kCompact && from == 0) {
             const int64_t m = ((int64_t)a.P + kApplyThreads - 1) / kApplyThreads;
@@ -584,11 +583,28 @@ cudaError_t launch(const PagesArgs &a, const li_page_pool *pools, int32_t n_pool
         attr[0].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        e = from == 0 ? cudaLaunchKernelEx(&cfg, apply_kernel<OP, true>, a, some)
-                      : cudaLaunchKernelEx(&cfg, apply_kernel<OP, false>, a, some);
+        e = from == 0 ? cudaLaunchKernelEx(&cfg, apply_kernel<OP, true, N>, a, some)
+                      : cudaLaunchKernelEx(&cfg, apply_kernel<OP, false, N>, a, some);
         ++*launches;
     }
     return e;
+}
+
+template <int OP>
+cudaError_t launch(const PagesArgs &a, const li_page_pool *pools, int32_t n_pools, cudaStream_t s, int *launches)
+{
+    const int sms = sm_count();
+    int copy_blocks = 0;
+    if (OP != kCompact && a.refs != a.refs_out) {
+        copy_blocks = (a.P + kPlanThreads - 1) / kPlanThreads;
+        if (copy_blocks > sms - 1) copy_blocks = sms - 1;
+    }
+    plan_kernel<OP><<<1 + copy_blocks, kPlanThreads, 0, s>>>(a);
+    const cudaError_t e = cudaGetLastError();
+    *launches = 1;
+    if (e != cudaSuccess) return e;
+    return n_pools <= kFewPools ? launch_apply<OP, kFewPools>(a, pools, n_pools, sms, s, launches)
+                                : launch_apply<OP, kMaxPools>(a, pools, n_pools, sms, s, launches);
 }
 
 // Checks shared by the calls that change the state, then the launches.
@@ -676,7 +692,7 @@ extern "C" LI_API li_status li_pages_copy(const li_pages_params *p, const li_pag
     int launches = 0;
     for (int32_t from = 0; from < n_pools; from += kMaxPools) {
         int64_t chunks;
-        const Pools some = some_pools(pools, from, n_pools, &chunks);
+        const Pools<kMaxPools> some = some_pools<kMaxPools>(pools, from, n_pools, &chunks);
         const int64_t items = chunks * n, blocks = items < 8LL * sms ? items : 8LL * sms;
         copy_kernel<<<(unsigned)blocks, kApplyThreads, 0, static_cast<cudaStream_t>(stream)>>>(
             src_pages, dst_pages, n, p->num_pages, status, some);

@@ -149,7 +149,7 @@ def _check(model, got, pools, status):
 
 
 SIZES = [  # seed, B, cols, page size, pages
-    (0, 4, 5, 16, 32), (1, 1, 1, 1, 1), (2, 37, 9, 48, 300), (3, 130, 33, 64, 5000), (4, 3, 700, 16, 40000), (5, 2000, 3, 128, 3500),
+    (0, 4, 5, 16, 32), (1, 1, 1, 1, 1), (2, 37, 9, 48, 300), (3, 130, 33, 64, 5000), (4, 3, 700, 16, 40000), (5, 2000, 3, 128, 3500), (6, 700, 400, 1, 9000),
 ]
 
 
