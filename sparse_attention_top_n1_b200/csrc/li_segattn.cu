@@ -497,7 +497,6 @@ segattn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_k, cons
                     uint32_t sq[2][16];
                     tmem_ld16(ts + side * 32, sq[0]);
                     tmem_ld16(ts + side * 32 + 16, sq[1]);
-                    if (k + 1 < mine) ahead = keys_of(u + 1);   // while the scores come
                     tmem_ld_wait16(sq[0]);
                     tmem_ld_wait16(sq[1]);
                     auto sv = [&](int j) -> uint32_t & { return sq[j >> 4][j & 15]; };
@@ -559,8 +558,8 @@ segattn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_k, cons
                 } else {
                     const uint32_t none[16] = {};
                     tmem_st16(ts + side * 16, none);
-                    if (k + 1 < mine) ahead = keys_of(u + 1);
                 }
+                if (k + 1 < mine) ahead = keys_of(u + 1);       // while the weights go
                 tmem_st_wait();
                 if (k == cut_tile) {
                     // values behind the last visible key: zeros
