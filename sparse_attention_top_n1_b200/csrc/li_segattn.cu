@@ -688,8 +688,9 @@ segattn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_k, cons
             for (int32_t k = 0; k < todo; ++k, ++u) {
                 const uint32_t st = u % NS, sb = u & 1;
                 wait_phase(&kfull[st], (u / NS) & 1, g.status, abort_flag);
-                // the buffer's last weights have been read
-                if (u >= 2) wait_phase(pvdone, u & 1, g.status, abort_flag);
+                // the buffer's last weights have been read (before a round's first tile
+                // all have: a wait for them now could take a later phase for theirs)
+                if (k > 0 && u >= 2) wait_phase(pvdone, u & 1, g.status, abort_flag);
                 tc_fence_after_sync();
                 __syncwarp();
                 if (leader) {
@@ -707,7 +708,12 @@ segattn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_k, cons
                 __syncwarp();
                 if (k > 0) weigh(u - 1);
             }
-            if (todo > 0) weigh(u - 1);
+            if (todo > 0) {
+                if (u >= 2) wait_phase(pvdone, u & 1, g.status, abort_flag);
+                __syncwarp();
+                weigh(u - 1);
+                wait_phase(pvdone, (u - 1) & 1, g.status, abort_flag);
+            }
             // a barrier of its own for the end: whoever waits for it late must not
             // take a later phase of pvdone for an earlier one
             if (next == kNone && leader) mma_commit(odone);

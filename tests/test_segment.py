@@ -154,6 +154,8 @@ CASES = {
     "more_rows_than_keys": dict(q_lens=[80], k_lens=[30], seg_size=16, seg_count=2),
     "steep": dict(q_lens=[33], k_lens=[500], softmax_scale=3.0, seg_count=4),
     "odd_group": dict(q_lens=[50], k_lens=[333], N1=21, N2=3, seg_count=3),
+    "many_windows": dict(q_lens=[100, 3], k_lens=[11200, 5000], N1=2, N2=2, D=64, seg_size=16, seg_count=40),
+    "full_list": dict(q_lens=[2], k_lens=[17000], N1=8, N2=1, seg_size=16, seg_count=1024, layout_kv="PA_BSND", block_size=48),
     "group_of_100": dict(q_lens=[11], k_lens=[333], N1=100, N2=1, seg_count=3, layout_kv="PA_BSND", block_size=256),
 }
 
@@ -237,6 +239,58 @@ def test_select_separates_scores_that_32_bits_would_not():
 
 
 @gpu
+@pytest.mark.parametrize("rows,ns", [(5, 300), (1, 4000)])
+def test_select_ranks_scores_near_the_border_in_64_bits(rows, ns):
+    """A dozen scores around the last one chosen differ by 2^-28 of their size,
+    less than the fast scores can tell: those chosen are the largest, and of two
+    equal ones the lower segment."""
+    p, x = sseg.make_segment(57, q_lens=[rows], k_lens=[ns * 16], sparse_mode=0, local_segs=0, init_segs=0, N1=2, N2=1, D=64,
+                             seg_size=16, seg_count=20)
+    g = torch.Generator().manual_seed(5)
+    x["query"] = torch.ones_like(x["query"])
+    at = torch.randperm(ns, generator=g)
+    pooled = torch.randn(1, ns, 1, 64, generator=g) * 0.01
+    pooled[0, at[:14], 0, 0] += 8.0                              # 14 clearly above, 12 at the border for 6 places
+    pooled[0, at[14:26], 0] = 0.0
+    pooled[0, at[14:26], 0, 0] = 4.0
+    step = torch.tensor([0, 5, 3, 3, 9, 1, 7, 7, 2, 8, 4, 6])
+    pooled[0, at[14:26], 0, 1] = step.float() * 2.0 ** -26
+    idx = _select(p, _dev(x), pooled.cuda())
+    assert np.array_equal(idx.cpu().numpy(), oseg.select(p, x, pooled))
+
+
+@gpu
+def test_select_of_zeros_and_of_many_rows():
+    """Means or queries of zero: every score is zero and the lowest segments are
+    chosen; rows enough for blocks of more than 16."""
+    p, x = sseg.make_segment(58, q_lens=[650, 650], k_lens=[3000, 2500], N1=8, N2=8, D=64, seg_size=32, seg_count=12)
+    x["query"][0, :40] = 0.0
+    g = torch.Generator().manual_seed(6)
+    pooled = torch.randn(p.B, p.max_segs, 8, 64, generator=g)
+    pooled[1] = 0.0
+    idx = _select(p, _dev(x), pooled.cuda())
+    assert np.array_equal(idx.cpu().numpy(), oseg.select(p, x, pooled))
+
+
+@gpu
+@pytest.mark.parametrize("value", [float("inf"), float("nan"), 1e38, 1e-30])
+def test_select_of_extreme_means(value):
+    """Scores that overflow, vanish or are not numbers in 32 bits are still chosen
+    as 64 bits choose (NaN counts as -inf)."""
+    p, x = sseg.make_segment(59, q_lens=[6], k_lens=[90 * 16], sparse_mode=0, local_segs=0, init_segs=0, N1=4, N2=2, D=64,
+                             seg_size=16, seg_count=9)
+    g = torch.Generator().manual_seed(7)
+    pooled = torch.randn(1, 90, 2, 64, generator=g)
+    if value == 1e-30:
+        pooled *= value
+    else:
+        pooled[0, 11, :, 3] = value
+        pooled[0, 50, :, 5] = -value
+    idx = _select(p, _dev(x), pooled.cuda())
+    assert np.array_equal(idx.cpu().numpy(), oseg.select(p, x, pooled))
+
+
+@gpu
 def test_select_cuts_at_max_segs_and_flags():
     p, x = sseg.make_segment(53, q_lens=[2], k_lens=[700], seg_size=64, max_segs=6, sparse_mode=0, local_segs=0, seg_count=3)
     st = torch.zeros(1, dtype=torch.int32, device="cuda")
@@ -264,7 +318,8 @@ def _chosen(p, x, seed, keep=0.5):
 
 
 @gpu
-@pytest.mark.parametrize("name", ["decode", "prefill", "prefill_mha", "tnd_paged", "pages_end_inside", "no_mask", "odd_group"])
+@pytest.mark.parametrize("name", ["decode", "prefill", "prefill_mha", "tnd_paged", "pages_end_inside", "no_mask", "odd_group",
+                                  "many_windows", "full_list"])
 def test_attention_on_any_choice_of_segments(name):
     """Not only what select gives: rows of a block that share nothing, rows with
     nothing, segments that a row does not see at all, holes."""
@@ -358,6 +413,40 @@ def test_bad_pages_are_skipped_and_flagged():
         else:
             want = np.zeros((4, p.D))
         assert np.all(np.abs(out[r].double().cpu().numpy() - want) <= (2 ** -7 + 2 ** -13) * 5)
+
+
+@gpu
+def test_attention_gives_the_same_bits_again_and_again():
+    """Many launches in a row: no wait runs into its limit, no bit changes."""
+    for name in ("tnd", "pages_end_inside", "prefill", "decode"):
+        p, x = _case(name)
+        d, idx = _dev(x), torch.from_numpy(_chosen(p, x, 12)).cuda()
+        first = _attend(p, d, idx)
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        pr = li.make_segment_params(p)
+        outs = [li.segment_attention(pr, d["query"], d["key"], d["value"], idx, status=st,
+                                     **_args(d, "act_seq_q", "act_seq_k", "block_table")) for _ in range(100)]
+        assert first[2] == 0 and int(st.item()) == 0
+        assert all(torch.equal(o, first[0]) and torch.equal(l, first[1]) for o, l in outs)
+
+
+@gpu
+def test_pools_with_pages_apart():
+    """kv_block_stride that is no multiple of a key row."""
+    p, x = sseg.make_segment(60, q_lens=[9, 2], k_lens=[300, 128], layout_kv="PA_BSND", block_size=64, N1=16, N2=2)
+    d = _dev(x)
+    n, page = p.num_blocks, 64 * 2 * 128
+    apart = []
+    for name in ("key", "value"):
+        wide = torch.full((n, page + 24), float("nan"), dtype=torch.bfloat16, device="cuda")
+        wide[:, :page] = d[name].view(n, page)
+        apart.append(wide.view(-1)[:n * (page + 24)].as_strided((n, 64, 2, 128), (page + 24, 256, 128, 1)))
+    p2 = sseg.SegmentProblem(**{**p.__dict__, "kv_block_stride": page + 24})
+    pooled = li.segment_pool(li.make_segment_params(p2), apart[0], **_args(d, "act_seq_k", "block_table"))
+    idx = _select(p, d, pooled)
+    a = _attend(p2, dict(d, key=apart[0], value=apart[1]), idx)
+    b = _attend(p, d, idx)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]) and a[2] == b[2] == 0
 
 
 @gpu
