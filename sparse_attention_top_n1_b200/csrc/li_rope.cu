@@ -31,6 +31,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kBatch = 4;              // units a thread has in flight
+constexpr int kStaged = 24576;         // bytes of heads that a block turns in shared memory at a time
 constexpr int kTable = 4096;           // (cos, sin) pairs of one block: 32 KB
 
 struct Head {                          // one tensor and its output
@@ -45,7 +46,8 @@ struct RopeArgs {
     const double *inv_freq;
     int32_t rows, N1, N2, D, half, off;     // half = rot_dim / 2
     int32_t row_tile, heads_per_block;
-    uint32_t mul_row, mul_head;             // ceil(2^32 / units of a row, of a head) (0: divide by one)
+    uint32_t mul_row, mul_head, mul_half;   // ceil(2^32 / units of a row, of a head, pairs of a head) (0: divide by one)
+    bool one_row;                           // (staged) blocks of one row
     float mscale, sin_sign;
     int32_t copy_rest;                      // out of place: columns outside the turned part
 };
@@ -68,6 +70,17 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float
 
 // u / d with m = ceil(2^32 / d), for u * d < 2^32
 __device__ __forceinline__ uint32_t quotient(uint32_t u, uint32_t m) { return m ? __umulhi(u, m) : u; }
+
+// cos and sin of pair e % half of row row0 + e / half
+__device__ __forceinline__ float2 angle(const RopeArgs &a, int64_t row0, int e)
+{
+    constexpr double kInvTwoPi = 0.15915494309189533576888;
+    const int r = e / a.half, p = e - r * a.half;
+    const double t = (double)a.positions[row0 + r] * (a.inv_freq[p] * kInvTwoPi);
+    float s, c;
+    sincospif(2.f * (float)(t - rint(t)), &s, &c);
+    return make_float2(c * a.mscale, s * a.mscale * a.sin_sign);
+}
 
 template <typename T, int V> union Vec {
     typename Raw<sizeof(T) * V>::T raw;
@@ -126,14 +139,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a)
         }
         if (base == 0) {
             // the block's angles, while the first loads are under way
-            constexpr double kInvTwoPi = 0.15915494309189533576888;
-            for (int e = tid; e < nrows * a.half; e += kThreads) {
-                const int r = e / a.half, p = e - r * a.half;
-                const double t = (double)a.positions[row0 + r] * (a.inv_freq[p] * kInvTwoPi);
-                float s, c;
-                sincospif(2.f * (float)(t - rint(t)), &s, &c);
-                table[e] = make_float2(c * a.mscale, s * a.mscale * a.sin_sign);
-            }
+            for (int e = tid; e < nrows * a.half; e += kThreads) table[e] = angle(a, row0, e);
             __syncthreads();
         }
 #pragma unroll
@@ -172,6 +178,98 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a)
     }
 }
 
+// Heads whose turned part does not start or split on 16 bytes, though the heads
+// themselves lie on them: whole heads come and go in 16-byte accesses, and the
+// pairs are turned in shared memory, where narrow accesses cost little (20000
+// rows of 72 heads of 128, 90 columns turned from column 30 on: 158 us, 404 us
+// with the 4-byte accesses that the pairs allow; 64 rows 3.4 and 4.2 us).
+template <typename T, bool HALF>
+__global__ void __launch_bounds__(kThreads) rope_staged_kernel(const RopeArgs a)
+{
+    constexpr int V = 16 / (int)sizeof(T);
+    extern __shared__ uint4 stage[];                    // [kStaged bytes], then the angles [row_tile][half]
+    float2 *table = reinterpret_cast<float2 *>(reinterpret_cast<char *>(stage) + kStaged);
+    const int tid = threadIdx.x;
+    const int64_t row0 = (int64_t)blockIdx.x * a.row_tile;
+    const int nrows = (int)(a.rows - row0 < a.row_tile ? a.rows - row0 : a.row_tile);
+    const int head0 = blockIdx.y * a.heads_per_block;
+    const int heads_all = a.N1 + a.N2;
+    const uint32_t nheads = (uint32_t)(heads_all - head0 < a.heads_per_block ? heads_all - head0 : a.heads_per_block);
+    const uint32_t vecs = (uint32_t)(a.D / V), n = nheads * (uint32_t)nrows;     // vectors of a head; heads of the block
+    const uint32_t most = (uint32_t)kStaged / 16 / vecs;
+    for (int e = tid; e < nrows * a.half; e += kThreads) table[e] = angle(a, row0, e);
+    for (uint32_t h0 = 0; h0 < n; h0 += most) {
+        const uint32_t cnt = n - h0 < most ? n - h0 : most;
+        auto place = [&](uint32_t e, bool in) -> uint4 * {     // vector e of these heads
+            const uint32_t hr = quotient(e, a.mul_head), c = e - hr * vecs;
+            const uint32_t r = a.one_row ? 0u : quotient(h0 + hr, a.mul_row);
+            const int h = head0 + (int)(h0 + hr - r * nheads);
+            const Head &t = h < a.N1 ? a.q : a.k;
+            const int hh = h < a.N1 ? h : h - a.N1;
+            const T *p = in ? static_cast<const T *>(t.in) + (row0 + r) * t.row + hh * t.head
+                            : static_cast<const T *>(t.out) + (row0 + r) * t.out_row + hh * t.out_head;
+            return reinterpret_cast<uint4 *>(const_cast<T *>(p)) + c;
+        };
+        for (uint32_t e0 = 0; e0 < cnt * vecs; e0 += kThreads * kBatch) {
+            uint4 x[kBatch];
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                const uint32_t e = e0 + j * kThreads + tid;
+                if (e < cnt * vecs) x[j] = __ldcs(place(e, true));
+            }
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                const uint32_t e = e0 + j * kThreads + tid;
+                if (e < cnt * vecs) stage[e] = x[j];
+            }
+        }
+        __syncthreads();
+        for (uint32_t u = tid; u < cnt * (uint32_t)a.half; u += kThreads) {
+            const uint32_t hr = quotient(u, a.mul_half), p = u - hr * a.half;
+            const uint32_t r = a.one_row ? 0u : quotient(h0 + hr, a.mul_row);
+            T *head = reinterpret_cast<T *>(stage) + hr * a.D + a.off;
+            T &e0 = head[HALF ? p : 2 * p], &e1 = head[HALF ? p + a.half : 2 * p + 1];
+            const float2 cs = table[r * a.half + p];
+            const float u0 = to_f<T>(e0), u1 = to_f<T>(e1);
+            e0 = from_f<T>(u0 * cs.x - u1 * cs.y);
+            e1 = from_f<T>(u1 * cs.x + u0 * cs.y);
+        }
+        __syncthreads();
+        for (uint32_t e = tid; e < cnt * vecs; e += kThreads) __stcs(place(e, false), stage[e]);
+        __syncthreads();
+    }
+}
+
+uint32_t magic(uint32_t d) { return d > 1 ? 0xFFFFFFFFu / d + 1 : 0u; }
+
+template <typename T, bool HALF>
+cudaError_t launch_staged(RopeArgs a, int sms, cudaStream_t s)
+{
+    const int64_t heads = a.N1 + a.N2, per_row = heads * a.D * (int64_t)sizeof(T);
+    int64_t tile = 2 * kStaged / per_row;               // two fillings of the stage
+    if (tile > kTable / 2 / a.half) tile = kTable / 2 / a.half;
+    if (tile > a.rows / (4 * sms)) tile = a.rows / (4 * sms);
+    if (tile < 1) tile = 1;
+    a.row_tile = (int)tile;
+    int64_t grid_x = (a.rows + tile - 1) / tile, grid_y = 1;
+    if (tile == 1) {
+        grid_y = 2 * sms / grid_x;
+        if (grid_y > heads) grid_y = heads;
+        if (grid_y < 1) grid_y = 1;
+    }
+    a.heads_per_block = (int)((heads + grid_y - 1) / grid_y);
+    grid_y = (heads + a.heads_per_block - 1) / a.heads_per_block;
+    a.mul_head = magic((uint32_t)(a.D * (int)sizeof(T) / 16));
+    a.mul_half = magic((uint32_t)a.half);
+    // of a block's last, shorter run of heads too: rows are counted by heads_per_block
+    // only when one block takes them all
+    a.mul_row = tile == 1 ? 0u : magic((uint32_t)a.heads_per_block);
+    a.one_row = tile == 1;
+    rope_staged_kernel<T, HALF><<<dim3((unsigned)grid_x, (unsigned)grid_y), kThreads,
+                                  kStaged + (size_t)tile * a.half * sizeof(float2), s>>>(a);
+    return cudaGetLastError();
+}
+
 template <typename T, int V, bool HALF>
 cudaError_t launch(RopeArgs a, int sms, cudaStream_t s)
 {
@@ -196,17 +294,18 @@ cudaError_t launch(RopeArgs a, int sms, cudaStream_t s)
     a.heads_per_block = (int)((heads + grid_y - 1) / grid_y);
     grid_y = (heads + a.heads_per_block - 1) / a.heads_per_block;
     const uint32_t head_units = (uint32_t)(a.half / kPairs), row_units = head_units * (uint32_t)a.heads_per_block;
-    a.mul_row = row_units > 1 ? (uint32_t)(0xFFFFFFFFu / row_units + 1) : 0u;
-    a.mul_head = head_units > 1 ? (uint32_t)(0xFFFFFFFFu / head_units + 1) : 0u;
+    a.mul_row = magic(row_units);
+    a.mul_head = magic(head_units);
     rope_kernel<T, V, HALF><<<dim3((unsigned)grid_x, (unsigned)grid_y), kThreads,
                               (size_t)tile * a.half * sizeof(float2), s>>>(a);
     return cudaGetLastError();
 }
 
 template <typename T>
-cudaError_t launch_t(const RopeArgs &a, bool half, int v, int sms, cudaStream_t s)
+cudaError_t launch_t(const RopeArgs &a, bool half, int v, bool staged, int sms, cudaStream_t s)
 {
     constexpr int kWide = 16 / (int)sizeof(T);
+    if (v < kWide && staged) return half ? launch_staged<T, true>(a, sms, s) : launch_staged<T, false>(a, sms, s);
     if (half) {
         if (v >= kWide) return launch<T, kWide, true>(a, sms, s);
         if (v >= 2) return launch<T, 2, true>(a, sms, s);
@@ -275,7 +374,9 @@ extern "C" LI_API li_status li_rope(const li_rope_params *p, const int32_t *posi
     if (p->rows == 0) return LI_OK;
     // the widest access that every address of the call is aligned to
     bits |= es * (uintptr_t)(a.q.row | a.q.head | a.q.out_row | a.q.out_head | a.k.row | a.k.head | a.k.out_row | a.k.out_head);
-    bits |= es * (uintptr_t)(p->D | p->rot_offset | (p->pairing == LI_ROPE_HALF ? p->rot_dim / 2 : p->rot_dim));
+    bits |= es * (uintptr_t)p->D;
+    const bool staged = bits % 16 == 0;                // whole heads may be read in 16-byte accesses
+    bits |= es * (uintptr_t)(p->rot_offset | (p->pairing == LI_ROPE_HALF ? p->rot_dim / 2 : p->rot_dim));
     int v = 1;
     while (v * es < 16 && bits % (2 * v * es) == 0) v *= 2;
     a.positions = positions;
@@ -293,9 +394,9 @@ extern "C" LI_API li_status li_rope(const li_rope_params *p, const int32_t *posi
     if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool half = p->pairing == LI_ROPE_HALF;
-    const cudaError_t e = p->dtype == LI_BF16   ? launch_t<__nv_bfloat16>(a, half, v, sms, s)
-                          : p->dtype == LI_FP16 ? launch_t<__half>(a, half, v, sms, s)
-                                                : launch_t<float>(a, half, v, sms, s);
+    const cudaError_t e = p->dtype == LI_BF16   ? launch_t<__nv_bfloat16>(a, half, v, staged, sms, s)
+                          : p->dtype == LI_FP16 ? launch_t<__half>(a, half, v, staged, sms, s)
+                                                : launch_t<float>(a, half, v, staged, sms, s);
     if (e != cudaSuccess) return bad(LI_ERR_CUDA, cudaGetErrorString(e));
     li::set_launch_count(1);
     return LI_OK;

@@ -170,6 +170,11 @@ CASES = [
     ("bf16", 3000, 1, 1, 64, 2, 0, "half", 0, 1.0),
     ("bf16", 2, 1024, 1024, 1024, 1024, 0, "half", 0, 1.0),
     ("fp16", 5000, 2, 0, 256, 252, 4, "interleaved", 0, 1.0),
+    ("bf16", 300, 40, 3, 128, 90, 31, "interleaved", 1, 1.1),  # whole heads aligned, the turned part not
+    ("fp32", 41, 9, 1, 1024, 1000, 5, "half", 0, 1.0),
+    ("fp16", 5000, 1, 1, 64, 30, 1, "half", 0, 1.0),
+    ("bf16", 1, 7, 2, 96, 50, 46, "half", 0, 1.0),
+    ("bf16", 2500, 3, 0, 8, 2, 5, "half", 0, 1.0),
 ]
 
 
