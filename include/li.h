@@ -451,7 +451,8 @@ LI_API li_status li_pages_compact(const li_pages_params *p, const li_page_pool *
  *   li_segment_attention  J = keys t < vis(r) of the selected segments;
  *                         out_h = sum_J softmax(softmax_scale q_h . k_t) v_t,
  *                         lse_h = log sum_J exp(softmax_scale q_h . k_t);
- *                         0 and -inf when J is empty, and for BSND padding rows.
+ *                         0 and -inf when J is empty, for BSND padding rows and
+ *                         for TND rows behind the last sequence (select: -1).
  *                         What a row does not select has no effect on it, not
  *                         even as a NaN or infinity.
  *

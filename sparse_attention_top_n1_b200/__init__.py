@@ -543,8 +543,12 @@ def _pages_state(params, table, lens, refs, out, workspace, status):
     if workspace is None:
         workspace = alloc_pages_workspace(p, table.device)
     state = _arg("table", table, d, i32, n), _arg("lens", lens, d, i32, B), _arg("refs", refs, d, i32, pages)
-    after = (_arg("table_out", out[0], d, i32, n), _arg("lens_out", out[1], d, i32, B),
-             _arg("refs_out", out[2], d, i32, pages))
+    to = out
+    if to[0] is table and to[1] is lens and to[2] is refs:               # in place: checked already
+        after = state
+    else:
+        after = (_arg("table_out", to[0], d, i32, n), _arg("lens_out", to[1], d, i32, B),
+                 _arg("refs_out", to[2], d, i32, pages))
     return d, out, state, after, (_opt("status", status, d, i32, 1), _arg("workspace", workspace, d, torch.uint8, None),
                                   workspace.numel())
 

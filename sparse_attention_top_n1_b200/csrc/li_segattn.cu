@@ -26,6 +26,17 @@
 //   warp 8     TMA: a key and a value box per quantum; empty slots take
 //              coordinates outside the tensor, which read as zeros
 //   warp 9     S = Q K^T one tile ahead of O += P V (P from tensor memory)
+// Two CTAs share an SM, one's softmax beside the other's products.  Bound by the
+// tensor core and what stands between its products: 4096 rows of 64 heads on 2
+// over 16384 keys, 2048 keys a row, take 490 us (0.56 PFLOP/s of what the rows
+// ask for, 0.99 of the union's tiles), a tile of 64 keys 900 cycles per SM, where
+// its products alone need 654 (128x64x16 with both operands in shared memory 49
+// cycles, 128x128x16 with the weights in tensor memory 65).  64 decode rows of 64
+// heads with 2048 keys each: 20 us, 25 us with the keys in HBM (67 MB: 10 us).
+// Measured and not taken: a score buffer less and the queries in tensor memory
+// (624 us); 2^x partly by a polynomial (no faster: the exponential is a third of
+// a tile's latency, not the limit); at most 64 rows twice in the tensor core with
+// the tiles in turn (24 us for the decode rows).
 // A key that a row does not take has weight 0 in it, but 0 * inf is NaN: values
 // behind the last key that the block sees are zeroed in shared memory, and a
 // result that is not finite although its sum of weights is, is computed again by
