@@ -371,6 +371,28 @@ segattn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_k, cons
             tmem = __shfl_sync(0xffffffffu, *tslot, 0);
         }
         auto entries = [&](int32_t r) { return a.idx + ((int64_t)(row0 + r) * g.N2 + n) * g.count; };
+        // 32 entries of a row, its last accepted one being `last`: which are accepted
+        // (existing, and above all before them), the last accepted one before each,
+        // and the last of all
+        auto accept = [&](int32_t s, int32_t last, bool &ok, int32_t &before, int32_t &top) {
+            const bool in = s >= 0 && s < segs;
+            before = __shfl_up_sync(0xffffffffu, s, 1);
+            if (lane == 0) before = last;
+            ok = in;
+            // as li_segment_select leaves them: ascending, no holes
+            if (__all_sync(0xffffffffu, s == -1 || (in && s > before && (before >= 0 || lane == 0)))) {
+                const uint32_t m = __ballot_sync(0xffffffffu, in);
+                top = m ? __shfl_sync(0xffffffffu, s, 31 - __clz(m)) : last;
+                return;
+            }
+            const int32_t upto = scan_max(in ? s : -1, lane);
+            before = __shfl_up_sync(0xffffffffu, upto, 1);
+            before = lane == 0 || before < last ? last : before;
+            ok = in && s > before;
+            if (s != -1 && !ok) seg_flag(g, LI_DEV_BAD_INDEX);
+            top = __shfl_sync(0xffffffffu, upto, 31);
+            top = top > last ? top : last;
+        };
         int32_t listed = 0;
         if (listed_alone) {
             if (warp == 0) {
@@ -378,55 +400,60 @@ segattn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_k, cons
                 int32_t last = -1;
                 for (int32_t e0 = 0; e0 < (vis > 0 ? g.count : 0); e0 += 32) {
                     const int32_t s = e0 + lane < g.count ? src[e0 + lane] : -1;
-                    const bool in = s >= 0 && s < segs;
-                    const int32_t upto = scan_max(in ? s : -1, lane);
-                    int32_t before = __shfl_up_sync(0xffffffffu, upto, 1);
-                    before = lane == 0 || before < last ? last : before;
-                    const bool ok = in && s > before;
-                    if (s != -1 && !ok) seg_flag(g, LI_DEV_BAD_INDEX);
+                    bool ok;
+                    int32_t before, top;
+                    accept(s, last, ok, before, top);
                     const bool use = ok && s * g.seg < vis;
                     const uint32_t m = __ballot_sync(0xffffffffu, use);
                     if (use) list[listed + __popc(m & ((1u << lane) - 1u))] = s;
                     listed += __popc(m);
-                    const int32_t top = __shfl_sync(0xffffffffu, upto, 31);
-                    last = top > last ? top : last;
+                    last = top;
                 }
                 if (lane == 0) *s_listed = listed;
             }
             __syncthreads();
             listed = *s_listed;
         } else {
-            for (int32_t r = warp; r < nr; r += kWarps) {
-                const int32_t vis = svis[r];
-                if (vis <= 0) continue;
-                const int32_t *src = entries(r);
-                int32_t at = cursor[r], last = lastof[r], next = kNone;
-                while (at < g.count) {
-                    const int32_t s = at + lane < g.count ? src[at + lane] : -1;
-                    const bool in = s >= 0 && s < segs;
-                    const int32_t upto = scan_max(in ? s : -1, lane);
-                    int32_t before = __shfl_up_sync(0xffffffffu, upto, 1);
-                    before = lane == 0 || before < last ? last : before;
-                    const bool ok = in && s > before;
-                    if (s != -1 && !ok) seg_flag(g, LI_DEV_BAD_INDEX);
-                    const bool use = ok && s * g.seg < vis;
-                    const uint32_t later = __ballot_sync(0xffffffffu, use && s - w0 >= W);
-                    const int end = later ? __ffs(later) - 1 : 32;
-                    if (use && lane < end) atomicOr(&member[(s - w0) * MW + (r >> 5)], 1u << (r & 31));
-                    if (later) {
-                        next = __shfl_sync(0xffffffffu, s, end);
-                        last = __shfl_sync(0xffffffffu, before, end);
-                        at += end;
-                        break;
-                    }
-                    const int32_t top = __shfl_sync(0xffffffffu, upto, 31);
-                    last = top > last ? top : last;
-                    at += 32;
+            // four rows' next entries are loaded at a time: one latency, not four
+            for (int32_t r0 = warp; r0 < nr; r0 += 4 * kWarps) {
+                int32_t ahead[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int32_t r = r0 + j * kWarps;
+                    ahead[j] = -1;
+                    if (r < nr && svis[r] > 0 && cursor[r] + lane < g.count) ahead[j] = entries(r)[cursor[r] + lane];
                 }
-                if (lane == 0) {
-                    cursor[r] = at;
-                    lastof[r] = last;
-                    if (next != kNone) atomicMin(s_next, next);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int32_t r = r0 + j * kWarps;
+                    if (r >= nr || svis[r] <= 0) continue;
+                    const int32_t *src = entries(r);
+                    const int32_t vis = svis[r];
+                    int32_t at = cursor[r], last = lastof[r], next = kNone, s = ahead[j];
+                    while (at < g.count) {
+                        const int32_t then = at + 32 + lane < g.count ? src[at + 32 + lane] : -1;
+                        bool ok;
+                        int32_t before, top;
+                        accept(s, last, ok, before, top);
+                        const bool use = ok && s * g.seg < vis;
+                        const uint32_t later = __ballot_sync(0xffffffffu, use && s - w0 >= W);
+                        const int end = later ? __ffs(later) - 1 : 32;
+                        if (use && lane < end) atomicOr(&member[(s - w0) * MW + (r >> 5)], 1u << (r & 31));
+                        if (later) {
+                            next = __shfl_sync(0xffffffffu, s, end);
+                            last = __shfl_sync(0xffffffffu, before, end);
+                            at += end;
+                            break;
+                        }
+                        last = top;
+                        at += 32;
+                        s = then;
+                    }
+                    if (lane == 0) {
+                        cursor[r] = at;
+                        lastof[r] = last;
+                        if (next != kNone) atomicMin(s_next, next);
+                    }
                 }
             }
             __syncthreads();
@@ -935,9 +962,12 @@ extern "C" LI_API li_status li_segment_attention(const li_segment_params *p, con
     if (es == LI_OK) es = li::tensor_map_16bit(&mv, value, 3, dims, strides, box, "segment values");
     if (es != LI_OK) return es;
     // CTAs per block: while the grid stays within one wave of two CTAs per SM
-    // and every CTA keeps two tiles of what a single row may take
+    // and every CTA keeps two tiles of what its rows may take
     const int64_t most = paged ? (int64_t)g.max_blocks_per_seq * g.block_size : (g.layout_kv == LI_BSND ? g.S2 : g.T2);
-    const int64_t keys = (int64_t)g.count * g.seg < most ? (int64_t)g.count * g.seg : most;
+    // (rows that share a block take about twice what one takes; 100 rows of 6
+    // segments: 14.4 us so, 16.5 us counted as one)
+    const bool shared = a.R > 1 && (g.layout_q == LI_BSND ? g.S1 > 1 : g.T1 > g.B);
+    const int64_t some = (int64_t)g.count * g.seg * (shared ? 2 : 1), keys = some < most ? some : most;
     const int64_t wave = 2LL * seg_sms();
     int split = 1;
     while (split < kMaxSplit && blocks * g.N2 * split * 2 <= wave && keys >= (int64_t)split * 2 * 2 * kTile) split *= 2;
