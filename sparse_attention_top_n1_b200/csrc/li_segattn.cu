@@ -28,8 +28,8 @@
 //   warp 9     S = Q K^T one tile ahead of O += P V (P from tensor memory)
 // Two CTAs share an SM, one's softmax beside the other's products.  Bound by the
 // tensor core and what stands between its products: 4096 rows of 64 heads on 2
-// over 16384 keys, 2048 keys a row, take 490 us (0.56 PFLOP/s of what the rows
-// ask for, 0.99 of the union's tiles), a tile of 64 keys 900 cycles per SM, where
+// over 16384 keys, 2048 keys a row, take 470 us (0.59 PFLOP/s of what the rows
+// ask for, 1.04 of the union's tiles), a tile of 64 keys 900 cycles per SM, where
 // its products alone need 654 (128x64x16 with both operands in shared memory 49
 // cycles, 128x128x16 with the weights in tensor memory 65).  64 decode rows of 64
 // heads with 2048 keys each: 20 us, 25 us with the keys in HBM (67 MB: 10 us).
@@ -618,7 +618,9 @@ segattn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_k, cons
         } else if (warp == kSoftWarps) {
             // ------------------------------------------------------------ copies
             const bool paged = g.layout_kv == LI_PA_BSND;
-            const uint64_t whole = Q == 64 ? ~0ull : (1ull << Q) - 1;
+            int32_t row_vis[4];                          // of rows lane, lane + 32, ...
+#pragma unroll
+            for (int i = 0; i < 4; ++i) row_vis[i] = svis[32 * i + lane];
             const int32_t batch = 32 / slots;            // tiles whose slots the warp's lanes hold
             int32_t mb = 0, t0 = -1, c1 = 0, c2 = a.no_page;
             // keys go a tile ahead of values, as the scores do
@@ -677,18 +679,23 @@ segattn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_k, cons
                 }
                 // the rows' masks; the entry's last reader, the softmax of tile u - RING, was
                 // done before the scores that this key stage has held since were issued
-                for (int32_t i = 0; i < MW; ++i) {
-                    const int32_t vis = svis[32 * i + lane];
-                    uint64_t m = 0;
-                    for (int32_t s = 0; s < slots; ++s) {
-                        const int32_t from = __shfl_sync(0xffffffffu, t0, j * slots + s);
-                        const int32_t at = __shfl_sync(0xffffffffu, mb, j * slots + s);
-                        if (from < 0) continue;
-                        const int32_t c = vis - from;
-                        if (c > 0 && (member[at + i] >> lane & 1u)) m |= (c >= Q ? whole : (1ull << c) - 1) << (s * Q);
+                uint64_t m[4] = {};
+                for (int32_t s = 0; s < slots; ++s) {
+                    const int32_t from = __shfl_sync(0xffffffffu, t0, j * slots + s);
+                    const int32_t at = __shfl_sync(0xffffffffu, mb, j * slots + s);
+                    if (from < 0) continue;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (i >= MW) break;
+                        const int32_t c = row_vis[i] - from;       // keys of the quantum that the row sees
+                        const int32_t cc = c < 1 ? 1 : (c < Q ? c : Q);
+                        const bool takes = (c > 0) & ((member[at + i] >> lane & 1u) != 0);
+                        m[i] |= takes ? ~0ull >> (64 - cc) << (s * Q) : 0ull;
                     }
-                    masks[u % L::RING * kM + 32 * i + lane] = m;
                 }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (i < MW) masks[u % L::RING * kM + 32 * i + lane] = m[i];
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&mfull[u % L::RING]);
                 if (k > 0) values(u - 1, v_my, v1, v2);
