@@ -194,6 +194,30 @@ def test_pages_match_the_model(op, seed, B, cols, ps, P, in_place):
 
 
 @pytest.mark.gpu
+def test_fork_of_whole_pages_beside_open_ones():
+    """Children of a row that ends with its last page copy nothing; the free pages,
+    page 0 among them, go to the others in order."""
+    ps, cols, P, B = 4, 5, 12, 9
+    table = np.full((B, cols), -1, np.int32)
+    table[0, :3], table[1, :2], table[2, :5] = [7, 3, 9], [5, 2], [11, 10, 8, 6, 4]
+    lens = np.array([9, 8, 17, 0, 0, 0, 0, 0, 0], np.int32)      # open, whole, open
+    refs = np.zeros(P, np.int32)
+    refs[[7, 3, 9, 5, 2, 11, 10, 8, 6, 4]] = 1
+    host = _pools(3, P, SHAPES)
+    model = oc.Pages(table, lens, refs, ps, [p.numpy() for p in host])
+    src, dst = [1, 0, 1, 2, 1], [4, 3, 8, 5, 6]
+    model.fork(src, dst)
+    assert model.flags == 0 and model.table[3][2] == 0 and model.table[5][4] == 1
+    d = [torch.from_numpy(t).cuda() for t in (table, lens, refs)]
+    pools = [p.cuda() for p in host]
+    pr = li.make_pages_params(num_pages=P, page_size=ps, max_pages_per_seq=cols, B=B)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    got = li.pages_fork(pr, pools, *d, i32(src), i32(dst), status=status)
+    _check(model, got, pools, status)
+
+
+@pytest.mark.gpu
 def test_pages_run_out_in_order():
     """Rows are served in order until the pages run out; the rest stay as they were."""
     table = np.full((5, 4), -1, np.int32)
