@@ -488,7 +488,8 @@ LI_API li_status li_pages_compact(const li_pages_params *p, const li_page_pool *
  *   status     as in li_sparse_attention
  * Pointers: query, key, value, out and pooled 16-byte aligned, the others
  * 4-byte.  Accumulation is fp32; the softmax weights enter the P.V product
- * rounded to dtype.  One launch each, no workspace.
+ * rounded to dtype and out is divided by the sum of those (lse holds the sum of
+ * the weights before rounding).  One launch each, no workspace.
  */
 typedef struct {
     int32_t layout_q, layout_kv;

@@ -21,15 +21,19 @@
 //              take the key, weights exp2(s - m) rounded to the input type back
 //              into tensor memory over the scores they came from; m moves only
 //              when a tile beats it by 2^8, and only then the two threads
-//              exchange their maxima and O is rescaled; the sum is of the weights
-//              before rounding, so lse is an fp32 result
+//              exchange their maxima and O is rescaled.  Two sums: of the weights
+//              as they are rounded, which O is divided by, so that equal values
+//              come out as they are (divided by the other sum they would be off
+//              by up to a rounding of the largest weight), and of the weights
+//              before that, so lse is an fp32 result
 //   warp 8     TMA: a key and a value box per quantum; empty slots take
 //              coordinates outside the tensor, which read as zeros
 //   warp 9     S = Q K^T one tile ahead of O += P V (P from tensor memory)
 // Two CTAs share an SM, one's softmax beside the other's products.  Bound by the
 // tensor core and what stands between its products: 4096 rows of 64 heads on 2
-// over 16384 keys, 2048 keys a row, take 470 us (0.59 PFLOP/s of what the rows
-// ask for, 1.04 of the union's tiles), a tile of 64 keys 900 cycles per SM, where
+// over 16384 keys, 2048 keys a row, take 485 us (0.57 PFLOP/s of what the rows
+// ask for, 1.01 of the union's tiles; 471 us with one sum of weights), a tile of
+// 64 keys 930 cycles per SM, where
 // its products alone need 654 (128x64x16 with both operands in shared memory 49
 // cycles, 128x128x16 with the weights in tensor memory 65).  64 decode rows of 64
 // heads with 2048 keys each: 20 us, 25 us with the keys in HBM (67 MB: 10 us).
@@ -99,7 +103,7 @@ struct Layout {
     static constexpr int VIS = LIST + kMember * 4;          // int32 [kM]
     static constexpr int CURSOR = VIS + kM * 4;             // int32 [kM]
     static constexpr int LAST = CURSOR + kM * 4;            // int32 [kM]
-    static constexpr int MERGE = MEMBER;                    // float [3][kM], when the tiles are done
+    static constexpr int MERGE = MEMBER;                    // float [3][kM], then [kM/C+1][C], when the tiles are done
     static constexpr int TOP = LAST + kM * 4;               // float [2][kM]: maxima, then sums, of the half rows
     static constexpr int RING = STAGES + 2;                 // tiles whose masks are held at a time
     static constexpr int MASK = TOP + 2 * kM * 4;           // uint64 [RING][kM]: the keys that a query row takes
@@ -355,7 +359,7 @@ segattn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_k, cons
     uint32_t tmem = 0;
     int32_t w0 = 0;
     uint32_t u = 0;                                      // tiles so far (every role counts alike)
-    float m_run = -INFINITY, l_run = 0.f;
+    float m_run = -INFINITY, l_run = 0.f, d_run = 0.f;   // maximum; sums of the weights, exact and as they enter P V
     for (bool first = true;; first = false) {
         // ---------------------------------------------------------------- plan
         if (!listed_alone)
@@ -565,7 +569,7 @@ segattn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_k, cons
                         }
                     }
                     const float mb = m_run == -INFINITY ? 0.f : -m_run;
-                    float rs[2][2] = {};
+                    float rs[2][2] = {}, rd[2][2] = {};
                     uint32_t pk[16];
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
@@ -576,8 +580,10 @@ segattn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_k, cons
                         x1 = ex2(x1);
                         pk[j] = pack2<F16>(x0, x1);
                         fadd2(rs[j & 1][0], rs[j & 1][1], x0, x1);
+                        fadd2(rd[j & 1][0], rd[j & 1][1], unpack_lo<F16>(pk[j]), unpack_hi<F16>(pk[j]));
                     }
                     l_run = l_run * alpha + ((rs[0][0] + rs[1][0]) + (rs[0][1] + rs[1][1]));
+                    d_run = d_run * alpha + ((rd[0][0] + rd[1][0]) + (rd[0][1] + rd[1][1]));
                     tmem_st16(ts + side * 16, pk);
                     if (u > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
                         wait_phase(pvdone, (u - 1) & 1, g.status, abort_flag);
@@ -779,8 +785,12 @@ segattn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_k, cons
         tops[side * kM + x] = l_run;
         pair_sync(1 + (warp & 3));
         l_run += tops[(side ^ 1) * kM + x];              // (of two summands: the same in both threads)
+        pair_sync(1 + (warp & 3));
+        tops[side * kM + x] = d_run;
+        pair_sync(1 + (warp & 3));
+        d_run += tops[(side ^ 1) * kM + x];
         float *sO = reinterpret_cast<float *>(base);     // [kM][D], 16-byte chunks of row r at c ^ (r & 15)
-        const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
+        const float inv = d_run == 0.f ? 0.f : 1.f / d_run;
         bool odd = false;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
@@ -818,30 +828,32 @@ segattn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_k, cons
             float *sM = reinterpret_cast<float *>(base + L::MERGE);
             sM[x] = m_run;
             sM[kM + x] = l_run;
+            sM[2 * kM + x] = d_run;
         }
     }
     if constexpr (C > 1) {
         // CTA `rank` merges its share of the tensor-core rows over the C partials
         float *sO = reinterpret_cast<float *>(base);
-        float *sM = reinterpret_cast<float *>(base + L::MERGE), *sL = sM + kM, *sWt = sL + kM;
+        float *sM = reinterpret_cast<float *>(base + L::MERGE), *sL = sM + kM, *sD = sL + kM;
         cooperative_groups::cluster_group cl = cooperative_groups::this_cluster();
         cl.sync();
         const int32_t share = (lanes + C - 1) / C, from = rank * share;
         const int32_t cnt = lanes - from < share ? (lanes > from ? lanes - from : 0) : share;
         auto out_at = [&](int32_t y) { return (int64_t)(row0 + y / g.G) * g.N1 + n * g.G + y % g.G; };
-        float *sums = sWt;                               // weight of partial r for row x: [share][C]
+        float *sums = sD + kM;                           // weight of partial r for row x: [share][C]
         for (int e = tid; e < cnt * C; e += kThreads) {
             const int y = from + e / C, r = e % C;
-            float top = -INFINITY, sum = 0.f;
+            float top = -INFINITY, sum = 0.f, div = 0.f;
 #pragma unroll
             for (int p = 0; p < C; ++p) top = fmaxf(top, cl.map_shared_rank(sM, p)[y]);
 #pragma unroll
             for (int p = 0; p < C; ++p) {
                 const float mp = cl.map_shared_rank(sM, p)[y], lp = cl.map_shared_rank(sL, p)[y];
-                if (lp != 0.f) sum += lp * (mp == -INFINITY ? 1.f : exp2f(mp - top));
+                const float f = mp == -INFINITY ? 1.f : exp2f(mp - top);
+                if (lp != 0.f) sum += lp * f, div += cl.map_shared_rank(sD, p)[y] * f;
             }
             const float mr = cl.map_shared_rank(sM, r)[y], lr = cl.map_shared_rank(sL, r)[y];
-            sums[e] = lr == 0.f ? 0.f : (mr == -INFINITY ? 1.f : exp2f(mr - top)) / sum;
+            sums[e] = lr == 0.f ? 0.f : (mr == -INFINITY ? 1.f : exp2f(mr - top)) / div;
             if (r == 0 && a.lse) a.lse[out_at(y)] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
         }
         __syncthreads();

@@ -366,6 +366,29 @@ def test_attention_is_blind_to_what_a_row_does_not_take(name, value):
 
 
 @gpu
+@pytest.mark.parametrize("name", ["decode", "decode_long", "prefill", "prefill_mha", "tnd", "no_mask", "odd_group"])
+def test_attention_of_equal_values_is_that_value(name):
+    """Values that are the same for every key of a head come out bit for bit: O is
+    divided by the sum of the weights that entered it.  Both sums hold at most 4480
+    terms of one sign here.  Products are exact and summed in 280 steps of 16, each
+    off by at most 2^-23 of the sum, weights in chains of 8 per tile of 64 and 70
+    tiles: less than 2^-14 in all, which is below half a step
+    (fp16 2^-12 of a value at the least, bf16 2^-9), so the result rounds to the
+    value.  The logits' spread (4 here) leaves a few weights that count, none of
+    them 1: the sum before rounding would be off by up to a rounding of those."""
+    p, x = _case(name, softmax_scale=4.0 * CASES[name].get("D", 128) ** -0.5)
+    v = torch.randn(p.N2, p.D, generator=torch.Generator().manual_seed(1)).to(x["value"].dtype)
+    v[:, ::4] = 2.0 - 2.0 * torch.finfo(v.dtype).eps              # nearest below 2 but one: its step is the smallest
+    x["value"][:] = v
+    idx = _chosen(p, x, 14, keep=0.8)
+    _, rlse = oseg.attention(p, x, idx)
+    out, lse, flags = _attend(p, _dev(x), torch.from_numpy(idx).cuda())
+    want = v.repeat_interleave(p.N1 // p.N2, 0).expand(p.rows, p.N1, p.D).clone()
+    want[torch.from_numpy(np.isneginf(rlse))] = 0.0
+    assert flags == 0 and torch.equal(out.cpu(), want)
+
+
+@gpu
 def test_attention_skips_and_flags_bad_entries():
     p, x = sseg.make_segment(54, q_lens=[40, 6], k_lens=[400, 100], N1=8, N2=2, seg_count=6, seg_size=64)
     idx = _chosen(p, x, 11, keep=1.0)
