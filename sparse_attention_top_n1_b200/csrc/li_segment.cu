@@ -384,8 +384,9 @@ __device__ bool choose(const SelRow &r, SelShared &sh, int team)
         }
     };
     // chosen: scores from `cut` on and above `over`; of those within [band_lo,
-    // band_hi] the ones that are `taken`
-    float cut = INFINITY, over = -INFINITY, band_lo = INFINITY, band_hi = -INFINITY;
+    // band_hi] the ones that are `taken`.  With nothing to choose, not even a score
+    // that has overflowed is above `over`.
+    float cut = INFINITY, over = need > 0 ? -INFINITY : INFINITY, band_lo = INFINITY, band_hi = -INFINITY;
     uint32_t taken = 0;
     int32_t ties = 0;                                  // equal scores of the cut that are chosen, lowest first (0: all)
     if (need > 0) {

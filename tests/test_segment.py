@@ -291,6 +291,23 @@ def test_select_of_extreme_means(value):
 
 
 @gpu
+@pytest.mark.parametrize("value", [1e38, -1e38, float("inf"), float("nan")])
+@pytest.mark.parametrize("ns", [5, 90, 300, 1000, 1500])
+def test_select_of_forced_segments_alone(ns, value):
+    """init_segs + local_segs = seg_count leaves nothing to choose: scores that
+    overflow 32 bits are not chosen, and nothing is written behind the row."""
+    p, x = sseg.make_segment(61, q_lens=[3], k_lens=[ns * 16], sparse_mode=0, init_segs=1, local_segs=1, N1=4, N2=2, D=64,
+                             seg_size=16, seg_count=2)
+    x["query"] = torch.ones_like(x["query"])
+    pooled = torch.full((1, ns, 2, 64), value)
+    n = p.rows * 2 * 2
+    wide = torch.full((n + 4096,), 77, dtype=torch.int32, device="cuda")
+    idx = _select(p, _dev(x), pooled.cuda(), out=wide[:n].view(p.rows, 2, 2))
+    assert bool((idx == torch.tensor([0, ns - 1], dtype=torch.int32, device="cuda")).all())
+    assert bool((wide[n:] == 77).all())
+
+
+@gpu
 def test_select_cuts_at_max_segs_and_flags():
     p, x = sseg.make_segment(53, q_lens=[2], k_lens=[700], seg_size=64, max_segs=6, sparse_mode=0, local_segs=0, seg_count=3)
     st = torch.zeros(1, dtype=torch.int32, device="cuda")
