@@ -413,9 +413,10 @@ def _torch_dtype(code):
     return torch.bfloat16 if code == 0 else torch.float16 if code == 1 else torch.float32
 
 
-def _launch(index, f, *args, stream=None):
+def _launch(index, f, *args, stream=None, held=None):
     """Call a library function for tensors on CUDA device `index`: the current
-    device and stream are that device's."""
+    device and stream are that device's.  `held`: memory that only this call
+    refers to, kept until its kernels are in the stream."""
     torch = _torch
     if index < 0:
         raise ValueError("the call's tensors must be on a CUDA device")
@@ -533,7 +534,8 @@ def _pools_on(pools, params, index):
 
 def _pages_state(params, table, lens, refs, out, workspace, status):
     """Checks the state, allocates what is not given; returns (device index, out,
-    pointers of the state, of the outputs, of status and the workspace)."""
+    pointers of the state, of the outputs, of status and the workspace, and the
+    workspace itself: to be held until the launch)."""
     torch = _load_torch()
     p, i32, d = params, torch.int32, table.get_device()
     B, pages = p.B, p.num_pages
@@ -550,7 +552,7 @@ def _pages_state(params, table, lens, refs, out, workspace, status):
         after = (_arg("table_out", to[0], d, i32, n), _arg("lens_out", to[1], d, i32, B),
                  _arg("refs_out", to[2], d, i32, pages))
     return d, out, state, after, (_opt("status", status, d, i32, 1), _arg("workspace", workspace, d, torch.uint8, None),
-                                  workspace.numel())
+                                  workspace.numel()), workspace
 
 
 def pages_copy(params: PagesParams, pools, src, dst, *, status=None, stream=None):
@@ -566,37 +568,38 @@ def pages_copy(params: PagesParams, pools, src, dst, *, status=None, stream=None
 def pages_reserve(params: PagesParams, table, lens, refs, new_lens, *, out=None, workspace=None, status=None, stream=None):
     """li_pages_reserve.  Returns (table, lens, refs) after the call: new
     tensors, or `out` (which may be the inputs, for in place)."""
-    d, out, state, after, rest = _pages_state(params, table, lens, refs, out, workspace, status)
+    d, out, state, after, rest, held = _pages_state(params, table, lens, refs, out, workspace, status)
     _launch(d, lib().li_pages_reserve, ctypes.byref(params), *state, _arg("new_lens", new_lens, d, _torch.int32, params.B),
-            *after, *rest, stream=stream)
+            *after, *rest, stream=stream, held=held)
     return out
 
 
 def pages_fork(params: PagesParams, pools, table, lens, refs, src_rows, dst_rows, *, out=None, workspace=None,
                status=None, stream=None):
     """li_pages_fork: row dst_rows[i] becomes a child of row src_rows[i]."""
-    d, out, state, after, rest = _pages_state(params, table, lens, refs, out, workspace, status)
+    d, out, state, after, rest, held = _pages_state(params, table, lens, refs, out, workspace, status)
     n, i32 = src_rows.numel(), _torch.int32
     s, t = _arg("src_rows", src_rows, d, i32, n), _arg("dst_rows", dst_rows, d, i32, n)
     arr = _pools_on(pools, params, d)
-    _launch(d, lib().li_pages_fork, ctypes.byref(params), arr, len(arr), *state, s, t, n, *after, *rest, stream=stream)
+    _launch(d, lib().li_pages_fork, ctypes.byref(params), arr, len(arr), *state, s, t, n, *after, *rest, stream=stream,
+            held=held)
     return out
 
 
 def pages_free(params: PagesParams, table, lens, refs, rows, *, out=None, workspace=None, status=None, stream=None):
     """li_pages_free: empties the rows `rows` (int32)."""
-    d, out, state, after, rest = _pages_state(params, table, lens, refs, out, workspace, status)
+    d, out, state, after, rest, held = _pages_state(params, table, lens, refs, out, workspace, status)
     n = rows.numel()
     _launch(d, lib().li_pages_free, ctypes.byref(params), *state, _arg("rows", rows, d, _torch.int32, n), n, *after, *rest,
-            stream=stream)
+            stream=stream, held=held)
     return out
 
 
 def pages_compact(params: PagesParams, pools, table, lens, refs, *, out=None, workspace=None, status=None, stream=None):
     """li_pages_compact: the live pages become the first ones of the pool."""
-    d, out, state, after, rest = _pages_state(params, table, lens, refs, out, workspace, status)
+    d, out, state, after, rest, held = _pages_state(params, table, lens, refs, out, workspace, status)
     arr = _pools_on(pools, params, d)
-    _launch(d, lib().li_pages_compact, ctypes.byref(params), arr, len(arr), *state, *after, *rest, stream=stream)
+    _launch(d, lib().li_pages_compact, ctypes.byref(params), arr, len(arr), *state, *after, *rest, stream=stream, held=held)
     return out
 
 
