@@ -192,6 +192,49 @@ def _stream(stream) -> Optional[int]:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
+_torch = None
+
+
+def _load_torch():
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
+class _Alloc:
+    """Allocations of one call on `device` that launches on `stream` (None: the
+    device's current one).  They come from the launch stream's memory, so that no
+    work of another stream is still under way in them; outputs are also marked as
+    used by the current stream, where the caller reads and frees them.  A
+    workspace has to be kept until after the launch."""
+
+    def __init__(self, stream, device):
+        torch = self.torch = _load_torch()
+        self.device, self.on = device, None
+        if stream is None or device.type != "cuda":
+            return
+        on = stream
+        if not hasattr(stream, "cuda_stream"):             # a raw handle; 0 is the default stream
+            on = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
+        reader = torch.cuda.current_stream(device)
+        if on.cuda_stream != reader.cuda_stream:
+            self.on, self.reader = on, reader
+
+    def workspace(self, *shape, dtype):
+        if self.on is None:
+            return self.torch.empty(shape, dtype=dtype, device=self.device)
+        with self.torch.cuda.stream(self.on):
+            return self.torch.empty(shape, dtype=dtype, device=self.device)
+
+    def output(self, *shape, dtype):
+        t = self.workspace(*shape, dtype=dtype)
+        if self.on is not None:
+            t.record_stream(self.reader)
+        return t
+
+
 def make_params(problem=None, **kw) -> Params:
     """Build li_params from an object with the attribute names of li_params
     (layouts and dtypes given as strings) and/or keyword overrides."""
@@ -296,10 +339,10 @@ def sparse_attention(params: SfaParams, query, key, value, sparse_indices, *, ac
                      act_seq_k=None, block_table=None, want_lse=True, status=None, stream=None):
     """Run li_sparse_attention, allocating out [rows, N1, Dv] (the query's dtype)
     and, when asked, lse [rows, N1] fp32.  Returns (out, lse or None)."""
-    import torch
     rows = params.B * params.S1 if params.layout_q == LAYOUT["BSND"] else params.T1
-    out = torch.empty((rows, params.N1, params.Dv), dtype=query.dtype, device=query.device)
-    lse = torch.empty((rows, params.N1), dtype=torch.float32, device=query.device) if want_lse else None
+    new = _Alloc(stream, query.device).output
+    out = new(rows, params.N1, params.Dv, dtype=query.dtype)
+    lse = new(rows, params.N1, dtype=_torch.float32) if want_lse else None
     li_sparse_attention(params, query, key, value, sparse_indices, act_seq_q, act_seq_k, block_table,
                         out, lse, status, stream)
     return out, lse
@@ -354,19 +397,17 @@ def indexer(params: Params, query, key, weights, *, act_seq_q=None, act_seq_k=No
     call.  Returns (sparse_indices, sparse_values); sparse_values is an empty
     (0,) tensor when return_value is 0, as the CANN guide's output rule says.
     """
-    import torch
     if cmp_residual_k is not None:
         params.cmp_residual_k = _ptr(cmp_residual_k)
     shape = li_output_shape(params)
-    dev = query.device
+    alloc = _Alloc(stream, query.device)
     if out is None:
-        idx = torch.empty(shape, dtype=torch.int32, device=dev)
-        val = (torch.empty(shape, dtype=torch.float32, device=dev) if params.return_value
-               else torch.empty((0,), dtype=torch.float32, device=dev))
+        idx = alloc.output(*shape, dtype=_torch.int32)
+        val = alloc.output(*(shape if params.return_value else (0,)), dtype=_torch.float32)
     else:
         idx, val = out
     if workspace is None:
-        workspace = alloc_workspace(params, dev)
+        workspace = alloc.workspace(max(li_workspace_size(params), 256), dtype=_torch.uint8)
     vptr = val if params.return_value else None
     if params.dtype_qk == DTYPE["e4m3"] or params.dtype_qk == DTYPE["int8"]:
         li_quant_indexer(params, query, key, weights, q_scale, k_scale, act_seq_q, act_seq_k,
@@ -378,17 +419,6 @@ def indexer(params: Params, query, key, weights, *, act_seq_q=None, act_seq_k=No
 
 
 # ---------------------------------------------------------------- rotary positions
-
-_torch = None
-
-
-def _load_torch():
-    global _torch
-    if _torch is None:
-        import torch
-        _torch = torch
-    return _torch
-
 
 def _arg(name, t, index, dtype, numel):
     """Pointer of a tensor argument, after its checks: on device `index`, of
@@ -471,12 +501,12 @@ def rope(params: RopeParams, positions, inv_freq, query, key=None, *, out=None, 
     nq = rows * p.N1 * D
     q = _arg("query", query, d, dt, None if p.q_row_stride or p.q_head_stride else nq)
     if out is None:
-        out = torch.empty((rows, p.N1, D), dtype=dt, device=query.device)
+        out = _Alloc(stream, query.device).output(rows, p.N1, D, dtype=dt)
     o = _arg("out", out, d, dt, None if p.q_out_row_stride or p.q_out_head_stride else nq)
     k = ko = None
     if key is not None:
         if key_out is None:
-            key_out = torch.empty((rows, p.N2, D), dtype=dt, device=query.device)
+            key_out = _Alloc(stream, query.device).output(rows, p.N2, D, dtype=dt)
         nk = rows * p.N2 * D
         k = _arg("key", key, d, dt, None if p.k_row_stride or p.k_head_stride else nk)
         ko = _arg("key_out", key_out, d, dt, None if p.k_out_row_stride or p.k_out_head_stride else nk)
@@ -532,7 +562,7 @@ def _pools_on(pools, params, index):
     return arr
 
 
-def _pages_state(params, table, lens, refs, out, workspace, status):
+def _pages_state(params, table, lens, refs, out, workspace, status, stream):
     """Checks the state, allocates what is not given; returns (device index, out,
     pointers of the state, of the outputs, of status and the workspace, and the
     workspace itself: to be held until the launch)."""
@@ -541,9 +571,10 @@ def _pages_state(params, table, lens, refs, out, workspace, status):
     B, pages = p.B, p.num_pages
     n = B * p.max_pages_per_seq
     if out is None:
-        out = (torch.empty_like(table), torch.empty_like(lens), torch.empty_like(refs))
+        new = _Alloc(stream, table.device).output
+        out = tuple(new(*t.shape, dtype=i32) for t in (table, lens, refs))
     if workspace is None:
-        workspace = alloc_pages_workspace(p, table.device)
+        workspace = _Alloc(stream, table.device).workspace(li_pages_workspace_size(p), dtype=torch.uint8)
     state = _arg("table", table, d, i32, n), _arg("lens", lens, d, i32, B), _arg("refs", refs, d, i32, pages)
     to = out
     if to[0] is table and to[1] is lens and to[2] is refs:               # in place: checked already
@@ -568,7 +599,7 @@ def pages_copy(params: PagesParams, pools, src, dst, *, status=None, stream=None
 def pages_reserve(params: PagesParams, table, lens, refs, new_lens, *, out=None, workspace=None, status=None, stream=None):
     """li_pages_reserve.  Returns (table, lens, refs) after the call: new
     tensors, or `out` (which may be the inputs, for in place)."""
-    d, out, state, after, rest, held = _pages_state(params, table, lens, refs, out, workspace, status)
+    d, out, state, after, rest, held = _pages_state(params, table, lens, refs, out, workspace, status, stream)
     _launch(d, lib().li_pages_reserve, ctypes.byref(params), *state, _arg("new_lens", new_lens, d, _torch.int32, params.B),
             *after, *rest, stream=stream, held=held)
     return out
@@ -577,7 +608,7 @@ def pages_reserve(params: PagesParams, table, lens, refs, new_lens, *, out=None,
 def pages_fork(params: PagesParams, pools, table, lens, refs, src_rows, dst_rows, *, out=None, workspace=None,
                status=None, stream=None):
     """li_pages_fork: row dst_rows[i] becomes a child of row src_rows[i]."""
-    d, out, state, after, rest, held = _pages_state(params, table, lens, refs, out, workspace, status)
+    d, out, state, after, rest, held = _pages_state(params, table, lens, refs, out, workspace, status, stream)
     n, i32 = src_rows.numel(), _torch.int32
     s, t = _arg("src_rows", src_rows, d, i32, n), _arg("dst_rows", dst_rows, d, i32, n)
     arr = _pools_on(pools, params, d)
@@ -588,7 +619,7 @@ def pages_fork(params: PagesParams, pools, table, lens, refs, src_rows, dst_rows
 
 def pages_free(params: PagesParams, table, lens, refs, rows, *, out=None, workspace=None, status=None, stream=None):
     """li_pages_free: empties the rows `rows` (int32)."""
-    d, out, state, after, rest, held = _pages_state(params, table, lens, refs, out, workspace, status)
+    d, out, state, after, rest, held = _pages_state(params, table, lens, refs, out, workspace, status, stream)
     n = rows.numel()
     _launch(d, lib().li_pages_free, ctypes.byref(params), *state, _arg("rows", rows, d, _torch.int32, n), n, *after, *rest,
             stream=stream, held=held)
@@ -597,7 +628,7 @@ def pages_free(params: PagesParams, table, lens, refs, rows, *, out=None, worksp
 
 def pages_compact(params: PagesParams, pools, table, lens, refs, *, out=None, workspace=None, status=None, stream=None):
     """li_pages_compact: the live pages become the first ones of the pool."""
-    d, out, state, after, rest, held = _pages_state(params, table, lens, refs, out, workspace, status)
+    d, out, state, after, rest, held = _pages_state(params, table, lens, refs, out, workspace, status, stream)
     arr = _pools_on(pools, params, d)
     _launch(d, lib().li_pages_compact, ctypes.byref(params), arr, len(arr), *state, *after, *rest, stream=stream, held=held)
     return out
@@ -656,7 +687,7 @@ def segment_pool(params: SegmentParams, key, *, act_seq_k=None, block_table=None
     if pooled is None:
         if first is not None:
             raise ValueError("first refreshes an existing pooled tensor: pass pooled")
-        pooled = torch.empty((p.B, p.max_segs, p.N2, p.D), dtype=torch.float32, device=key.device)
+        pooled = _Alloc(stream, key.device).output(p.B, p.max_segs, p.N2, p.D, dtype=torch.float32)
     _, lens, table, st = _segment_lens(p, d, None, act_seq_k, block_table, status)
     _launch(d, lib().li_segment_pool, ctypes.byref(p), k, lens, table, _opt("first", first, d, torch.int32, p.B),
             _arg("pooled", pooled, d, torch.float32, p.B * p.max_segs * p.N2 * p.D), st, stream=stream)
@@ -672,7 +703,7 @@ def segment_select(params: SegmentParams, query, pooled, *, act_seq_q=None, act_
     rows, N2, D, count = _segment_rows(p), p.N2, p.D, p.seg_count
     q = _arg("query", query, d, _torch_dtype(p.dtype), rows * p.N1 * D)
     if out is None:
-        out = torch.empty((rows, N2, count), dtype=torch.int32, device=query.device)
+        out = _Alloc(stream, query.device).output(rows, N2, count, dtype=torch.int32)
     q_lens, k_lens, _, st = _segment_lens(p, d, act_seq_q, act_seq_k, None, status)
     _launch(d, lib().li_segment_select, ctypes.byref(p), q, _arg("pooled", pooled, d, torch.float32, p.B * p.max_segs * N2 * D),
             q_lens, k_lens, _arg("out", out, d, torch.int32, rows * N2 * count), st, stream=stream)
@@ -689,9 +720,9 @@ def segment_attention(params: SegmentParams, query, key, value, seg_idx, *, act_
     n = rows * N1 * D
     q, k, v = (_arg("query", query, d, dt, n), _arg("key", key, d, dt, keys), _arg("value", value, d, dt, keys))
     if out is None:
-        out = torch.empty((rows, N1, D), dtype=dt, device=query.device)
+        out = _Alloc(stream, query.device).output(rows, N1, D, dtype=dt)
     if lse is None and want_lse:
-        lse = torch.empty((rows, N1), dtype=torch.float32, device=query.device)
+        lse = _Alloc(stream, query.device).output(rows, N1, dtype=torch.float32)
     q_lens, k_lens, table, st = _segment_lens(p, d, act_seq_q, act_seq_k, block_table, status)
     _launch(d, lib().li_segment_attention, ctypes.byref(p), q, k, v,
             _arg("seg_idx", seg_idx, d, torch.int32, rows * p.N2 * p.seg_count), q_lens, k_lens, table,
