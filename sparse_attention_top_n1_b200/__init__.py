@@ -523,7 +523,8 @@ def make_pages_params(**kw) -> PagesParams:
 
 def page_pools(pools):
     """Descriptors of pool tensors [num_pages, ...] (axis 0 may be strided, a
-    page itself is contiguous), for the pages calls; they take a list too."""
+    page itself is contiguous and overlaps no other), for the pages calls; they
+    take a list too."""
     if isinstance(pools, ctypes.Array):
         return pools
     arr = (PagePool * len(pools))()
@@ -534,9 +535,11 @@ def page_pools(pools):
         each = t.numel() // n if n else 0
         if n and not t.is_contiguous() and not t[0].is_contiguous():
             raise ValueError("a pool's pages must be contiguous")
+        if n > 1 and t.stride(0) < each:
+            raise ValueError("a pool's pages overlap: %d elements apart, %d in each" % (t.stride(0), each))
         d.base = t.data_ptr()
         d.page_bytes = each * es
-        d.page_stride = max(t.stride(0) * es, each * es)
+        d.page_stride = (t.stride(0) if n > 1 else each) * es
     arr.tensors = list(pools)
     return arr
 

@@ -107,6 +107,26 @@ def test_wrapper_refuses_wrong_state():
         li.page_pools([torch.zeros(64, 16, 4).transpose(1, 2)])
 
 
+@pytest.mark.parametrize("stride", [0, 1, 8, 63])
+def test_pools_of_overlapping_pages_are_refused(stride):
+    """Their stride is not that of pages side by side: page n - 1 would be looked
+    for behind the tensor."""
+    t = torch.zeros(6 * 64, dtype=torch.int16)
+    with pytest.raises(ValueError, match="overlap"):
+        li.page_pools([t.as_strided((6, 16, 4), (stride, 4, 1))])
+    if stride == 0:
+        with pytest.raises(ValueError, match="overlap"):
+            li.page_pools([t[:64].expand(6, 64)])
+
+
+def test_descriptors_of_pools():
+    t = torch.zeros(6, 3, 64, dtype=torch.int16)
+    for pool, want in ((t, (384, 384)), (t[:, 1], (128, 384)), (t[:1, 1], (128, 128)), (t[::2], (384, 768)),
+                       (t.view(-1)[:64].expand(1, 64), (128, 128)), (t.view(-1).as_strided((1, 64), (5, 1)), (128, 128))):
+        d = li.page_pools([pool])[0]
+        assert d.base == pool.data_ptr() and (d.page_bytes, d.page_stride) == want
+
+
 # ------------------------------------------------------------------ GPU
 
 def _state(g, B, cols, ps, P, fill=0.5, shared=0.0):
