@@ -434,6 +434,16 @@ def _arg(name, t, index, dtype, numel):
     return t.data_ptr()
 
 
+def _strided(name, t, index, dtype, extent):
+    """The same for a tensor whose strides the parameters say: `extent` elements
+    from its first one on have to lie in its memory."""
+    p = _arg(name, t, index, dtype, None)
+    room = t.untyped_storage().nbytes() // t.element_size() - t.storage_offset()
+    if room < extent:
+        raise ValueError("%s has %d elements of memory, the call's strides reach over %d" % (name, room, extent))
+    return p
+
+
 def _opt(name, t, index, dtype, numel):
     return None if t is None else _arg(name, t, index, dtype, numel)
 
@@ -498,18 +508,22 @@ def rope(params: RopeParams, positions, inv_freq, query, key=None, *, out=None, 
     torch = _load_torch()
     p, d, dt = params, query.get_device(), _torch_dtype(params.dtype)
     rows, D = p.rows, p.D
-    nq = rows * p.N1 * D
-    q = _arg("query", query, d, dt, None if p.q_row_stride or p.q_head_stride else nq)
+
+    def arg(name, t, N, row, head):
+        if not row and not head:
+            return _arg(name, t, d, dt, rows * N * D)
+        last = (rows - 1) * (row or N * D) + (N - 1) * (head or D)
+        return _strided(name, t, d, dt, last + D if rows > 0 else 0)
+    q = arg("query", query, p.N1, p.q_row_stride, p.q_head_stride)
     if out is None:
         out = _Alloc(stream, query.device).output(rows, p.N1, D, dtype=dt)
-    o = _arg("out", out, d, dt, None if p.q_out_row_stride or p.q_out_head_stride else nq)
+    o = arg("out", out, p.N1, p.q_out_row_stride, p.q_out_head_stride)
     k = ko = None
     if key is not None:
         if key_out is None:
             key_out = _Alloc(stream, query.device).output(rows, p.N2, D, dtype=dt)
-        nk = rows * p.N2 * D
-        k = _arg("key", key, d, dt, None if p.k_row_stride or p.k_head_stride else nk)
-        ko = _arg("key_out", key_out, d, dt, None if p.k_out_row_stride or p.k_out_head_stride else nk)
+        k = arg("key", key, p.N2, p.k_row_stride, p.k_head_stride)
+        ko = arg("key_out", key_out, p.N2, p.k_out_row_stride, p.k_out_head_stride)
     _launch(d, lib().li_rope, ctypes.byref(p), _arg("positions", positions, d, torch.int32, rows),
             _arg("inv_freq", inv_freq, d, torch.float64, p.rot_dim // 2), q, k, o, ko, stream=stream)
     return out, key_out
@@ -660,11 +674,14 @@ def _segment_rows(p):
     return p.B * p.S1 if p.layout_q == 0 else p.T1
 
 
-def _segment_keys(p):
-    """Elements of the key (and value) tensor, or None for a strided pool."""
-    if p.layout_kv == 2:
-        return None if p.kv_block_stride else p.num_blocks * p.block_size * p.N2 * p.D
-    return (p.B * p.S2 if p.layout_kv == 0 else p.T2) * p.N2 * p.D
+def _segment_keys(name, t, p, index):
+    """Pointer of the key (or value) tensor, after its checks."""
+    dt, row = _torch_dtype(p.dtype), p.N2 * p.D
+    if p.layout_kv != 2:
+        return _arg(name, t, index, dt, (p.B * p.S2 if p.layout_kv == 0 else p.T2) * row)
+    if not p.kv_block_stride:
+        return _arg(name, t, index, dt, p.num_blocks * p.block_size * row)
+    return _strided(name, t, index, dt, (p.num_blocks - 1) * p.kv_block_stride + p.block_size * row)
 
 
 def _segment_lens(p, index, act_seq_q, act_seq_k, block_table, status):
@@ -686,7 +703,7 @@ def segment_pool(params: SegmentParams, key, *, act_seq_k=None, block_table=None
     (undefined in a newly allocated one)."""
     torch = _load_torch()
     p, d = params, key.get_device()
-    k = _arg("key", key, d, _torch_dtype(p.dtype), _segment_keys(p))
+    k = _segment_keys("key", key, p, d)
     if pooled is None:
         if first is not None:
             raise ValueError("first refreshes an existing pooled tensor: pass pooled")
@@ -719,9 +736,9 @@ def segment_attention(params: SegmentParams, query, key, value, seg_idx, *, act_
     when asked, lse [rows, N1] fp32.  Returns (out, lse or None)."""
     torch = _load_torch()
     p, d, dt = params, query.get_device(), _torch_dtype(params.dtype)
-    rows, keys, N1, D = _segment_rows(p), _segment_keys(p), p.N1, p.D
+    rows, N1, D = _segment_rows(p), p.N1, p.D
     n = rows * N1 * D
-    q, k, v = (_arg("query", query, d, dt, n), _arg("key", key, d, dt, keys), _arg("value", value, d, dt, keys))
+    q, k, v = _arg("query", query, d, dt, n), _segment_keys("key", key, p, d), _segment_keys("value", value, p, d)
     if out is None:
         out = _Alloc(stream, query.device).output(rows, N1, D, dtype=dt)
     if lse is None and want_lse:

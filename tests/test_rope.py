@@ -130,6 +130,26 @@ def test_wrapper_refuses_wrong_tensors():
         li.rope(pr, pos, f, q)                                  # host tensors
 
 
+@pytest.mark.parametrize("field,reach", [
+    ("q_row_stride", 7 * 600 + 512), ("q_head_stride", 7 * 1024 + 3 * 130 + 128), ("q_out_row_stride", 7 * 600 + 512),
+    ("q_out_head_stride", 7 * 1024 + 3 * 130 + 128), ("k_row_stride", 7 * 600 + 256), ("k_out_row_stride", 7 * 600 + 256),
+    ("k_head_stride", 7 * 1024 + 130 + 128), ("k_out_head_stride", 7 * 1024 + 130 + 128)])
+def test_wrapper_refuses_strides_that_leave_the_memory(field, reach):
+    """A row stride of 600, or heads 130 apart in rows of 1024: the last element
+    that the call reaches is the last one of the tensor, or one behind it."""
+    row = 600 if "row" in field else 1024
+    kw = {field: row if "row" in field else 130, field.replace("head", "row"): row}
+    pr = _pr(N2=2, **kw)
+    pos, f = torch.zeros(8, dtype=torch.int32), torch.zeros(32, dtype=torch.float64)
+    t = {n: torch.zeros(8, h, 128, dtype=torch.bfloat16) for n, h in (("query", 4), ("key", 2), ("out", 4), ("key_out", 2))}
+    name = {"q_out": "out", "k_out": "key_out"}.get(field[:5], "query" if field[0] == "q" else "key")
+    for short, match in ((0, "CUDA device"), (1, "%s has %d elements of memory" % (name, reach - 1))):
+        # a view from element 8 on of a longer tensor: what lies before it does not count
+        t[name] = torch.zeros(8 + reach - short, dtype=torch.bfloat16)[8:]
+        with pytest.raises(ValueError, match=match):
+            li.rope(pr, pos, f, **t)
+
+
 # ------------------------------------------------------------------ GPU
 
 def _tolerance(x, rot, off, pairing, m, dt):

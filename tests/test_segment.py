@@ -97,6 +97,22 @@ def test_wrapper_refuses_wrong_tensors():
             bad()
 
 
+@pytest.mark.parametrize("name", ["key", "value"])
+def test_wrapper_refuses_pools_shorter_than_their_stride_says(name):
+    pr = _pr(layout_kv="PA_BSND", num_blocks=4, block_size=32, max_blocks_per_seq=2, kv_block_stride=32 * 256 + 8)
+    reach = 3 * (32 * 256 + 8) + 32 * 256
+    t = {n: torch.zeros(reach, dtype=torch.bfloat16) for n in ("key", "value")}
+    q, idx = torch.zeros(2, 8, 8, 128, dtype=torch.bfloat16), torch.zeros(16, 2, 4, dtype=torch.int32)
+    for short, match in ((0, "CUDA device"), (1, "%s has %d elements of memory" % (name, reach - 1))):
+        t[name] = torch.zeros(24 + reach - short, dtype=torch.bfloat16)[24:]
+        calls = [lambda: li.segment_attention(pr, q, t["key"], t["value"], idx)]
+        if name == "key":
+            calls.append(lambda: li.segment_pool(pr, t["key"]))
+        for call in calls:
+            with pytest.raises(ValueError, match=match):
+                call()
+
+
 # ------------------------------------------------------------------ GPU
 
 def _dev(x):
