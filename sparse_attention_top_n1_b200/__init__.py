@@ -599,7 +599,7 @@ def _pages_state(params, table, lens, refs, out, workspace, status, stream):
     else:
         after = (_arg("table_out", to[0], d, i32, n), _arg("lens_out", to[1], d, i32, B),
                  _arg("refs_out", to[2], d, i32, pages))
-    return d, out, state, after, (_opt("status", status, d, i32, 1), _arg("workspace", workspace, d, torch.uint8, None),
+    return d, out, state, after, (_opt("status", status, d, i32, 1), _arg("workspace", workspace, d, torch.uint8, workspace.numel()),
                                   workspace.numel()), workspace
 
 

@@ -107,6 +107,17 @@ def test_wrapper_refuses_wrong_state():
         li.page_pools([torch.zeros(64, 16, 4).transpose(1, 2)])
 
 
+def test_wrapper_refuses_a_workspace_with_gaps():
+    """Its size counts elements; the calls write that many bytes in a row."""
+    pr = _pr()
+    t, n, r = (torch.zeros(s, dtype=torch.int32) for s in ((4, 8), (4,), (64,)))
+    ws = torch.empty(2 * li.li_pages_workspace_size(pr), dtype=torch.uint8)
+    with pytest.raises(ValueError, match="workspace must be contiguous"):
+        li.pages_reserve(pr, t, n, r, n, workspace=ws[::2])
+    with pytest.raises(ValueError, match="CUDA device"):
+        li.pages_reserve(pr, t, n, r, n, workspace=ws[:len(ws) // 2])
+
+
 @pytest.mark.parametrize("stride", [0, 1, 8, 63])
 def test_pools_of_overlapping_pages_are_refused(stride):
     """Their stride is not that of pages side by side: page n - 1 would be looked
