@@ -300,7 +300,8 @@ LI_API li_status li_sparse_attention(const li_sfa_params *p, const void *query, 
  * mscale it takes an output's gradient to the input's.
  *
  *   dtype         LI_BF16, LI_FP16 or LI_FP32: query, key and outputs
- *   rows          token rows (B*S1 or T1); 0 does nothing
+ *   rows          token rows (B*S1 or T1); 0 does nothing (the tensors' pointers
+ *                 may then be NULL)
  *   N1, N2        query heads 1..1024; key heads 0..1024 (0: no key, key pointers NULL)
  *   D             head dim 2..1024
  *   rot_dim       even, 2..D; rot_offset >= 0; rot_offset + rot_dim <= D

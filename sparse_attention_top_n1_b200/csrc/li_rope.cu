@@ -330,7 +330,7 @@ extern "C" LI_API li_status li_rope(const li_rope_params *p, const int32_t *posi
                                     void *stream)
 {
     li::set_launch_count(0);
-    if (!p || !positions || !inv_freq || !query || !query_out) return bad(LI_ERR_NULL, "a required pointer is NULL");
+    if (!p) return bad(LI_ERR_NULL, "params is NULL");
     if (p->reserved != 0) return bad(LI_ERR_SHAPE, "reserved must be 0");
     if (p->dtype != LI_BF16 && p->dtype != LI_FP16 && p->dtype != LI_FP32)
         return bad(LI_ERR_DTYPE, "dtype must be LI_BF16, LI_FP16 or LI_FP32");
@@ -344,8 +344,6 @@ extern "C" LI_API li_status li_rope(const li_rope_params *p, const int32_t *posi
     if (p->rot_dim < 2 || p->rot_dim % 2 || p->rot_offset < 0 || p->rot_dim > p->D || p->rot_offset > p->D - p->rot_dim)
         return bad(LI_ERR_SHAPE, "rot_dim must be even and rot_offset + rot_dim within the head");
     if (!(p->mscale > 0.f) || !std::isfinite(p->mscale)) return bad(LI_ERR_SHAPE, "mscale must be positive and finite");
-    if ((p->N2 > 0) != (key != nullptr) || (p->N2 > 0) != (key_out != nullptr))
-        return bad(LI_ERR_NULL, "key and key_out go with N2 > 0");
     RopeArgs a{};
     auto head = [&](const void *in, void *out, int n, int64_t row, int64_t hd, int64_t orow, int64_t ohd, Head &t) {
         t.in = in;
@@ -362,6 +360,10 @@ extern "C" LI_API li_status li_rope(const li_rope_params *p, const int32_t *posi
         (p->N2 && !head(key, key_out, p->N2, p->k_row_stride, p->k_head_stride, p->k_out_row_stride,
                         p->k_out_head_stride, a.k)))
         return bad(LI_ERR_SHAPE, "strides let heads or rows overlap");
+    if (p->rows == 0) return LI_OK;                    // empty tensors have no address
+    if (!positions || !inv_freq || !query || !query_out) return bad(LI_ERR_NULL, "a required pointer is NULL");
+    if ((p->N2 > 0) != (key != nullptr) || (p->N2 > 0) != (key_out != nullptr))
+        return bad(LI_ERR_NULL, "key and key_out go with N2 > 0");
     const bool q_in = query == query_out, k_in = p->N2 == 0 || key == key_out;
     if ((q_in && (a.q.row != a.q.out_row || a.q.head != a.q.out_head)) ||
         (p->N2 && k_in && (a.k.row != a.k.out_row || a.k.head != a.k.out_head)))
@@ -371,7 +373,6 @@ extern "C" LI_API li_status li_rope(const li_rope_params *p, const int32_t *posi
                      reinterpret_cast<uintptr_t>(key) | reinterpret_cast<uintptr_t>(key_out);
     if (bits % es || reinterpret_cast<uintptr_t>(positions) % 4 || reinterpret_cast<uintptr_t>(inv_freq) % 8)
         return bad(LI_ERR_SHAPE, "a pointer is not aligned to its element");
-    if (p->rows == 0) return LI_OK;
     // the widest access that every address of the call is aligned to
     bits |= es * (uintptr_t)(a.q.row | a.q.head | a.q.out_row | a.q.out_head | a.k.row | a.k.head | a.k.out_row | a.k.out_head);
     bits |= es * (uintptr_t)p->D;

@@ -130,6 +130,14 @@ def test_wrapper_refuses_wrong_tensors():
         li.rope(pr, pos, f, q)                                  # host tensors
 
 
+def test_rope_of_no_rows_needs_no_tensors():
+    """Empty tensors have no address; the parameters are checked all the same."""
+    def call(**kw):
+        return li.STATUS_NAMES[li.lib().li_rope(ctypes.byref(_pr(rows=0, **kw)), None, None, None, None, None, None, None)]
+    assert call() == call(N2=2) == call(q_out_row_stride=1024) == "LI_OK" and li.li_last_launch_count() == 0
+    assert call(rot_dim=63) == call(q_row_stride=511) == "LI_ERR_SHAPE"
+
+
 @pytest.mark.parametrize("field,reach", [
     ("q_row_stride", 7 * 600 + 512), ("q_head_stride", 7 * 1024 + 3 * 130 + 128), ("q_out_row_stride", 7 * 600 + 512),
     ("q_out_head_stride", 7 * 1024 + 3 * 130 + 128), ("k_row_stride", 7 * 600 + 256), ("k_out_row_stride", 7 * 600 + 256),
@@ -217,6 +225,16 @@ def test_rope_matches_64_bits(dtype, rows, N1, N2, D, rot, off, pairing, inverse
         x64 = x.double().numpy()
         ref = oc.rope(x64, pos.numpy(), f.numpy(), rot, off, pairing, bool(inverse), m32)
         _check(y.double().cpu().numpy(), ref, x64, rot, off, pairing, m32, dtype)
+
+
+@pytest.mark.gpu
+def test_rope_of_an_empty_step():
+    e = lambda n: torch.empty(0, n, 128, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    pos, f = torch.empty(0, dtype=torch.int32, device="cuda"), li.rope_frequencies(64)[0].cuda()
+    out, kout = li.rope(_pr(rows=0, N2=2), pos, f, e(4), e(2))
+    assert out.shape == (0, 4, 128) and kout.shape == (0, 2, 128) and li.li_last_launch_count() == 0
+    q = e(4)
+    assert li.rope(_pr(rows=0, q_row_stride=1000, q_out_row_stride=1000), pos, f, q, out=q)[0] is q
 
 
 @pytest.mark.gpu
