@@ -487,6 +487,9 @@ LI_API li_status li_pages_compact(const li_pages_params *p, const li_page_pool *
  *              row is skipped and flagged with LI_DEV_BAD_INDEX
  *   out        [rows, N1, D] dtype; lse fp32 [rows, N1] or NULL
  *   status     as in li_sparse_attention
+ * No query rows: select and attention do nothing.  No keys (S2 or T2 of 0):
+ * pool does nothing, attention writes 0 and -inf.  Pointers of tensors without
+ * elements may be NULL.
  * Pointers: query, key, value, out and pooled 16-byte aligned, the others
  * 4-byte.  Accumulation is fp32; the softmax weights enter the P.V product
  * rounded to dtype and out is divided by the sum of those (lse holds the sum of

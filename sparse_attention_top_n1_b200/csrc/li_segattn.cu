@@ -939,11 +939,12 @@ extern "C" LI_API li_status li_segment_attention(const li_segment_params *p, con
     AttnArgs a{};
     const li_status st = seg_setup(call, p, true, true, act_seq_q, act_seq_k, block_table, status, &a.g);
     if (st != LI_OK) return st;
+    if (a.g.rows == 0) return LI_OK;                     // empty tensors have no address
+    if (seg_no_keys(a.g)) key = value = query;           // to have one: nothing is read there
     if (!query || !key || !value || !seg_idx || !out)
         return seg_fail(call, LI_ERR_NULL, "query, key, value, seg_idx and out are required");
     if (off(query, 16) || off(key, 16) || off(value, 16) || off(out, 16) || off(seg_idx, 4) || off(lse, 4))
         return seg_fail(call, LI_ERR_SHAPE, "query, key, value and out must be 16-byte aligned, seg_idx and lse 4-byte");
-    if (a.g.rows == 0) return LI_OK;
     a.q = static_cast<const uint16_t *>(query);
     a.k = static_cast<const uint16_t *>(key);
     a.v = static_cast<const uint16_t *>(value);

@@ -920,6 +920,7 @@ extern "C" LI_API li_status li_segment_pool(const li_segment_params *p, const vo
     SegGeo g{};
     const li_status st = seg_setup(call, p, false, true, nullptr, act_seq_k, block_table, status, &g);
     if (st != LI_OK) return st;
+    if (seg_no_keys(g)) return LI_OK;                        // no segment holds a key
     if (!key || !pooled) return seg_fail(call, LI_ERR_NULL, "key and pooled are required");
     if (off(key, 16) || off(pooled, 16) || off(first, 4))
         return seg_fail(call, LI_ERR_SHAPE, "key and pooled must be 16-byte aligned, first 4-byte");
@@ -948,10 +949,10 @@ extern "C" LI_API li_status li_segment_select(const li_segment_params *p, const 
     SelArgs a{};
     const li_status st = seg_setup(call, p, true, false, act_seq_q, act_seq_k, nullptr, status, &a.g);
     if (st != LI_OK) return st;
+    if (a.g.rows == 0) return LI_OK;                         // empty tensors have no address
     if (!query || !pooled || !seg_idx) return seg_fail(call, LI_ERR_NULL, "query, pooled and seg_idx are required");
     if (off(query, 16) || off(pooled, 16) || off(seg_idx, 4))
         return seg_fail(call, LI_ERR_SHAPE, "query and pooled must be 16-byte aligned, seg_idx 4-byte");
-    if (a.g.rows == 0) return LI_OK;
     a.q = static_cast<const uint16_t *>(query);
     a.pooled = pooled;
     a.idx = seg_idx;

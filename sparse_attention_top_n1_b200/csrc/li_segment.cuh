@@ -114,6 +114,11 @@ template <bool F16> __device__ __forceinline__ float seg_hi(uint32_t v)
 li_status seg_setup(const char *call, const li_segment_params *p, bool queries, bool keys, const int32_t *act_q,
                     const int32_t *act_k, const int32_t *block_table, int32_t *status, SegGeo *g);
 li_status seg_fail(const char *call, li_status st, const char *what);
+// The key tensor has no elements (and, in torch, no address).
+inline bool seg_no_keys(const SegGeo &g)
+{
+    return (g.layout_kv == LI_BSND && g.S2 == 0) || (g.layout_kv == LI_TND && g.T2 == 0);
+}
 int seg_sms();
 // A tensor map over 16-bit elements with the 128-byte swizzle; zeros outside.
 li_status tensor_map_16bit(CUtensorMap *m, const void *base, int rank, const uint64_t *dims, const uint64_t *strides_bytes,

@@ -97,6 +97,27 @@ def test_wrapper_refuses_wrong_tensors():
             bad()
 
 
+EMPTY = [dict(S1=0), dict(layout_q="TND", layout_kv="TND", T1=0, T2=64), dict(S2=0),
+         dict(layout_q="TND", layout_kv="TND", T1=5, T2=0), dict(S1=0, S2=0), dict(layout_q="TND", layout_kv="TND")]
+
+
+@pytest.mark.parametrize("kw", EMPTY)
+def test_empty_tensors_have_no_address(kw):
+    pr = _pr(**kw)
+    L, p = li.lib(), ctypes.byref(pr)
+    rows, keys = (pr.B * pr.S1, pr.B * pr.S2) if pr.layout_q == 0 else (pr.T1, pr.T2)
+    if not rows:
+        assert li.STATUS_NAMES[L.li_segment_select(p, None, FAKE, FAKE, FAKE, None, None, None)] == "LI_OK"
+        k = FAKE if keys else None
+        assert li.STATUS_NAMES[L.li_segment_attention(p, None, k, k, None, FAKE, FAKE, None, None, None, None, None)] == "LI_OK"
+    if not keys:
+        assert li.STATUS_NAMES[L.li_segment_pool(p, None, FAKE, None, None, FAKE, None, None)] == "LI_OK"
+        if rows:                                                  # keys are not what is missing
+            st = L.li_segment_attention(p, FAKE, None, None, FAKE, FAKE, FAKE, None, None, None, None, None)
+            assert li.STATUS_NAMES[st] == "LI_ERR_NULL"
+    assert li.li_last_launch_count() == 0
+
+
 @pytest.mark.parametrize("name", ["key", "value"])
 def test_wrapper_refuses_pools_shorter_than_their_stride_says(name):
     pr = _pr(layout_kv="PA_BSND", num_blocks=4, block_size=32, max_blocks_per_seq=2, kv_block_stride=32 * 256 + 8)
@@ -204,6 +225,29 @@ def test_pool_select_attention_match_the_oracle(name):
     out, lse, flags = _attend(p, d, idx)
     assert li.li_last_launch_count() == 1
     _compare(p, x, out, lse, idx.cpu().numpy(), 0, flags)
+
+
+@gpu
+@pytest.mark.parametrize("kw", EMPTY)
+def test_calls_without_rows_or_without_keys(kw):
+    pr = _pr(**kw)
+    tnd = pr.layout_q == 1
+    e = lambda *s: torch.empty(*s, dtype=torch.bfloat16, device="cuda").normal_()  # noqa: E731
+    q = e(pr.T1, 8, 128) if tnd else e(2, pr.S1, 8, 128)
+    k = e(pr.T2, 2, 128) if tnd else e(2, pr.S2, 2, 128)
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    aq, ak = (i32(pr.T1 // 2, pr.T1), i32(pr.T2 // 2, pr.T2)) if tnd else (None, None)
+    pooled = torch.full((2, 4, 2, 128), 7.0, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    li.segment_pool(pr, k, act_seq_k=ak, pooled=pooled, status=st)
+    assert bool((pooled == 7.0).all()) == (k.numel() == 0)
+    idx = li.segment_select(pr, q, pooled, act_seq_q=aq, act_seq_k=ak, status=st)
+    out, lse = li.segment_attention(pr, q, k, k, idx, act_seq_q=aq, act_seq_k=ak, status=st)
+    rows = q.numel() // (8 * 128)
+    assert idx.shape == (rows, 2, 4) and out.shape == (rows, 8, 128) and lse.shape == (rows, 8)
+    assert int(st.item()) == 0
+    if not k.numel():
+        assert bool((idx == -1).all()) and bool((out == 0).all()) and bool(torch.isneginf(lse).all())
 
 
 @gpu
