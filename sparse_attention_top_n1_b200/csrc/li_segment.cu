@@ -248,10 +248,10 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t 
     lo = *reinterpret_cast<const uint32_t *>(&l);
 }
 
-// Order of 64-bit scores as unsigned integers (NaN lowest, -0 = +0).
+// Order of 64-bit scores as unsigned integers (NaN = -inf, -0 = +0).
 __device__ __forceinline__ uint64_t order_of(double x)
 {
-    if (x != x) return 0;
+    if (x != x) x = -INFINITY;
     const uint64_t u = (uint64_t)__double_as_longlong(x + 0.0);
     return u >> 63 ? ~u : u | 0x8000000000000000ull;
 }

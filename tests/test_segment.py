@@ -351,6 +351,27 @@ def test_select_of_extreme_means(value):
 
 
 @gpu
+@pytest.mark.parametrize("ns", [12, 90, 700, 1500])
+def test_select_ties_nan_with_minus_infinity(ns):
+    """Where the choice reaches into scores of -inf, a NaN is one of them: the
+    lower segment is taken, whichever it is."""
+    p, x = sseg.make_segment(62, q_lens=[3], k_lens=[ns * 16], sparse_mode=0, local_segs=0, init_segs=0, N1=4, N2=2, D=64,
+                             seg_size=16, seg_count=9)
+    x["query"] = torch.ones_like(x["query"])
+    g = torch.Generator().manual_seed(8)
+    pooled = torch.randn(1, ns, 2, 64, generator=g)
+    pooled[0, :, 0, 3] = -float("inf")
+    pooled[0, ::2, 0, 5] = float("nan")                          # head 0: NaN and -inf in turn
+    pooled[0, :, 1, 3] = float("nan")
+    pooled[0, ::2, 1] = 0.0
+    pooled[0, ::2, 1, 3] = -float("inf")                         # head 1: -inf and NaN
+    for s in (ns - 3, ns - 6):                                   # and two numbers
+        pooled[0, s] = 1.0
+    idx = _select(p, _dev(x), pooled.cuda())
+    assert np.array_equal(idx.cpu().numpy(), oseg.select(p, x, pooled))
+
+
+@gpu
 @pytest.mark.parametrize("value", [1e38, -1e38, float("inf"), float("nan")])
 @pytest.mark.parametrize("ns", [5, 90, 300, 1000, 1500])
 def test_select_of_forced_segments_alone(ns, value):
