@@ -382,10 +382,12 @@ LI_API li_status li_rope_frequencies(int32_t scaling, int32_t rot_dim, double ba
  *                     destinations are distinct and no destination is a source
  *                     of another pair (else their contents are undefined)
  *
- * When the free pages run out, the rows (pairs) from the first that no longer
- * fits are left as they were and LI_DEV_NO_PAGES is flagged.  A row outside
- * [0, B), a row named twice (the first counts), a fork onto a row that is not
- * empty: skipped, LI_DEV_BAD_ROW.  A length outside [0, max_pages_per_seq *
+ * When the free pages run out, the rows (pairs) that need a fresh page are left
+ * as they were from the first that no longer fits on, and LI_DEV_NO_PAGES is
+ * flagged; those that need none (a row that grows inside its last page, a child
+ * of whole pages) are served wherever they stand.  A row outside [0, B), a row
+ * named twice (the first counts), a fork onto a row that is not empty: skipped,
+ * LI_DEV_BAD_ROW.  A length outside [0, max_pages_per_seq *
  * page_size]: the present length is clamped, a new one skipped,
  * LI_DEV_BAD_KLEN.  A page number outside [0, num_pages), a page whose count
  * would fall below 0: skipped (-1 in a written row), LI_DEV_BAD_BLOCK.
@@ -399,7 +401,7 @@ LI_API li_status li_rope_frequencies(int32_t scaling, int32_t rot_dim, double ba
  *              aligned, not shared by calls that may run at the same time
  * Two launches (li_pages_copy: one; one more per 64 pools beyond the first 64).
  */
-#define LI_DEV_NO_PAGES      0x40  /* pages: the free pages ran out (rows left as they were) */
+#define LI_DEV_NO_PAGES      0x40  /* pages: the free pages ran out (rows that need one left as they were) */
 #define LI_DEV_BAD_ROW       0x80  /* pages: a row out of range, named twice, or not empty (skipped) */
 typedef struct {
     int32_t num_pages, page_size, max_pages_per_seq, B;

@@ -272,6 +272,31 @@ def test_pages_run_out_in_order():
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("in_place", [False, True])
+def test_rows_that_need_no_page_are_served_when_pages_have_run_out(in_place):
+    """Behind the first row that no longer fits: a row that grows inside its last
+    page and a child of whole pages are served, a row that would fit is not."""
+    ps, P = 8, 7
+    table = np.array([[0, -1, -1, -1], [1, 2, -1, -1], [3, -1, -1, -1], [4, -1, -1, -1], [-1] * 4, [-1] * 4, [-1] * 4], np.int32)
+    lens, refs = np.array([8, 16, 3, 8, 0, 0, 0], np.int32), np.array([1, 1, 1, 1, 1, 0, 0], np.int32)
+    pr = li.make_pages_params(num_pages=P, page_size=ps, max_pages_per_seq=4, B=7)
+    i32 = lambda v: torch.tensor(np.asarray(v), dtype=torch.int32, device="cuda")  # noqa: E731
+    for op, a0, a1, want in (("reserve", [9, 32, 7, 9, 0, 1, 0], None, [9, 16, 7, 8, 0, 0, 0]),
+                             ("fork", [2, 2, 2, 1], [4, 5, 6, 3], None), ("fork", [1, 2, 0], [4, 5, 6], [8, 16, 3, 8, 16, 3, 8])):
+        model = oc.Pages(table, lens, refs, ps)
+        d, st = [i32(t) for t in (table, lens, refs)], torch.zeros(1, dtype=torch.int32, device="cuda")
+        out = tuple(d) if in_place else None
+        if op == "reserve":
+            model.reserve(a0)
+            got = li.pages_reserve(pr, *d, i32(a0), out=out, status=st)
+        else:
+            model.fork(a0, a1)
+            got = li.pages_fork(pr, [], *d, i32(a0), i32(a1), out=out, status=st)
+        _check(model, got, [], st)
+        assert want is None or got[1].tolist() == want
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("in_place", [False, True])
 def test_pages_bad_arguments_are_skipped_and_flagged(in_place):
     ps, P = 4, 12
     table = np.array([[1, 3, 99], [5, -1, -1], [-1] * 3, [-1] * 3, [7, 2, -1]], np.int32)
