@@ -436,7 +436,8 @@ extern "C" LI_API li_status li_rope_frequencies(int32_t scaling, int32_t rot_dim
         if (scaling == LI_ROPE_SCALE_LINEAR) {
             inv_freq[p] = f / factor;
         } else if (scaling == LI_ROPE_SCALE_YARN) {
-            const double keep = 1.0 - std::fmin(std::fmax((p - lo) / std::fmax(hi - lo, 0.001), 0.0), 1.0);
+            // (hi <= lo = 0 when even the first pair turns beta_slow times at most)
+            const double keep = p >= hi ? 0.0 : 1.0 - std::fmin(std::fmax((p - lo) / std::fmax(hi - lo, 0.001), 0.0), 1.0);
             inv_freq[p] = f * keep + f / factor * (1.0 - keep);
         } else {
             inv_freq[p] = f;

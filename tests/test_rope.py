@@ -45,6 +45,21 @@ def test_frequencies_follow_the_formulas():
     assert abs(m - (0.1 * math.log(16) + 1)) < 1e-6
 
 
+@pytest.mark.parametrize("rot,positions,fast,slow,base", [
+    (64, 4, 32.0, 1.0, 1e4), (2, 6, 32.0, 1.0, 1e4), (64, 1, 0.5, 0.2, 1e4), (64, 100, 40.0, 16.0, 1e4), (128, 7, 32.0, 1.0, 1e4),
+    (64, 1 << 20, 32.0, 1.0, 1e4), (4, 2 ** 31 - 1, 32.0, 1.0, 1e4), (2, 1 << 20, 32.0, 1.0, 2.0), (64, 4096, 32.0, 1.0, 2.0),
+    (64, 4096, 32.0, 1.0, 10.0)])
+def test_yarn_keeps_and_divides_by_the_number_of_turns(rot, positions, fast, slow, base):
+    """Pairs that turn beta_fast times and more are kept, those that turn beta_slow
+    times and less are divided, the first one among them where positions are few."""
+    f = li.rope_frequencies(rot, base, "yarn", 8.0, positions, fast, slow)[0].numpy()
+    plain = base ** (-2 * np.arange(rot // 2) / rot)
+    turns = positions * plain / (2 * math.pi)
+    assert np.allclose(f[turns >= fast], plain[turns >= fast], rtol=1e-15)
+    assert np.allclose(f[turns <= slow], plain[turns <= slow] / 8, rtol=1e-15)
+    assert np.all(f >= plain / 8 * (1 - 1e-15)) and np.all(f <= plain * (1 + 1e-15))
+
+
 def test_frequencies_of_one_pair_and_factor_one():
     for s in ("none", "linear"):
         f, m = li.rope_frequencies(2, 10000.0, s, 3.0)
