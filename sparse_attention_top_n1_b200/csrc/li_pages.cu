@@ -7,8 +7,9 @@
 // and ranks free or live pages by warp votes, so the result is the lowest
 // pages first whatever the timing.  Its other blocks copy the counts to the
 // output buffer meanwhile.  The apply kernel writes the new table, lengths and
-// counts and copies page contents; it is launched programmatically, so its
-// blocks are resident when the plan ends.
+// counts and copies page contents; it is launched programmatically, so that its
+// launch is prepared beside the plan, but the plan gives no signal before its
+// end and the apply's blocks start when the plan's have all exited.
 //
 // Bounds: the tables are a few hundred kilobytes, so small calls are bound by
 // the latency of two dependent launches and one scan (5 to 7 us; one launch of a
