@@ -457,7 +457,10 @@ LI_API li_status li_pages_compact(const li_pages_params *p, const li_page_pool *
  *                         0 and -inf when J is empty, for BSND padding rows and
  *                         for TND rows behind the last sequence (select: -1).
  *                         What a row does not select has no effect on it, not
- *                         even as a NaN or infinity.
+ *                         even as a NaN or infinity.  (Time it does cost: results
+ *                         that a value which is not finite reached, a row's own
+ *                         or a neighbour's, are computed again key by key, about
+ *                         0.36 us a key for each of a block's up to 128.)
  *
  *   layout_q, layout_kv   as li_sfa_params, with N2 key heads: key and value
  *                         [B,S2,N2,D], [T2,N2,D] or [num_blocks,block_size,N2,D]

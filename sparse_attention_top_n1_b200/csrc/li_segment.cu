@@ -172,8 +172,8 @@ __global__ void __launch_bounds__(kPoolThreads) pool_kernel(const SegGeo g, cons
                     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        acc[2 * e] += seg_lo<F16>(w[e]);
-                        acc[2 * e + 1] += seg_hi<F16>(w[e]);
+                        acc[2 * e] += unpack_lo<F16>(w[e]);
+                        acc[2 * e + 1] += unpack_hi<F16>(w[e]);
                     }
                     ++seen;
                 }
@@ -689,8 +689,8 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelArgs a)
                     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        acc[2 * k] += (double)seg_lo<F16>(w[k]);
-                        acc[2 * k + 1] += (double)seg_hi<F16>(w[k]);
+                        acc[2 * k] += (double)unpack_lo<F16>(w[k]);
+                        acc[2 * k + 1] += (double)unpack_hi<F16>(w[k]);
                     }
                 }
             }

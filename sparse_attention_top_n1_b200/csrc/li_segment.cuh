@@ -98,17 +98,6 @@ __device__ __forceinline__ int64_t seg_key_offset(const SegGeo &g, int32_t b, in
     return id * g.page_stride + (int64_t)in * row_elems;
 }
 
-template <bool F16> __device__ __forceinline__ float seg_lo(uint32_t v)
-{
-    if constexpr (F16) return __half2float(__ushort_as_half((unsigned short)(v & 0xFFFFu)));
-    else return __uint_as_float(v << 16);
-}
-template <bool F16> __device__ __forceinline__ float seg_hi(uint32_t v)
-{
-    if constexpr (F16) return __half2float(__ushort_as_half((unsigned short)(v >> 16)));
-    else return __uint_as_float(v & 0xFFFF0000u);
-}
-
 // Checks the parameters that the three calls share and fills the geometry.
 // `queries`: the call has query rows.  Returns LI_OK or reports `call`: reason.
 li_status seg_setup(const char *call, const li_segment_params *p, bool queries, bool keys, const int32_t *act_q,

@@ -7,11 +7,11 @@ so the mean is off by at most (n + 1) * 2^-24 * mean |key|.  Select: whole
 numbers, equal (the scores differ by 2^-50 relative; the inputs are random, so
 nothing lies that near the border, and exact ties are equal on both sides).
 Attention: the weights enter the P.V product rounded to the input type (half a
-step u = eps/2 each) and are normalised by the unrounded sum, and the weight of
-a single key can itself be off by one such rounding; the output rounds once
-more: |out - ref| <= 2u max|v| + u |ref| plus fp32 terms: the logit is off by
-at most D * 2^-24 * sum |q k| * scale, which is below 2^-13 here and enters
-relative to the weights.  lse has only the fp32 terms.
+step u = eps/2 each) and are normalised by the sum of those, which is off by one
+such rounding at the most; the output rounds once more: |out - ref| <= 2u max|v|
++ u |ref| plus fp32 terms: the logit is off by at most D * 2^-24 * sum |q k| *
+scale, which is below 2^-13 here and enters relative to the weights.  lse has
+only the fp32 terms.
 """
 from __future__ import annotations
 
