@@ -501,6 +501,12 @@ def li_rope(params: RopeParams, positions, inv_freq, query, key, query_out, key_
                          _ptr(query_out), _ptr(key_out), _stream(stream)))
 
 
+def _heads(name, t, index, dtype, p, N, row, head):
+    """Pointer of N heads per row at the given strides (0: dense)."""
+    last = (p.rows - 1) * (row or N * p.D) + (N - 1) * (head or p.D)
+    return _strided(name, t, index, dtype, last + p.D if p.rows > 0 else 0)
+
+
 def rope(params: RopeParams, positions, inv_freq, query, key=None, *, out=None, key_out=None, stream=None):
     """Rotate query [.., N1, D] and key [.., N2, D] by their rows' positions,
     allocating dense outputs unless they are given (query and key themselves for
@@ -508,22 +514,22 @@ def rope(params: RopeParams, positions, inv_freq, query, key=None, *, out=None, 
     torch = _load_torch()
     p, d, dt = params, query.get_device(), _torch_dtype(params.dtype)
     rows, D = p.rows, p.D
-
-    def arg(name, t, N, row, head):
-        if not row and not head:
-            return _arg(name, t, d, dt, rows * N * D)
-        last = (rows - 1) * (row or N * D) + (N - 1) * (head or D)
-        return _strided(name, t, d, dt, last + D if rows > 0 else 0)
-    q = arg("query", query, p.N1, p.q_row_stride, p.q_head_stride)
+    nq = rows * p.N1 * D
+    q = (_heads("query", query, d, dt, p, p.N1, p.q_row_stride, p.q_head_stride) if p.q_row_stride or p.q_head_stride
+         else _arg("query", query, d, dt, nq))
     if out is None:
         out = _Alloc(stream, query.device).output(rows, p.N1, D, dtype=dt)
-    o = arg("out", out, p.N1, p.q_out_row_stride, p.q_out_head_stride)
+    o = (_heads("out", out, d, dt, p, p.N1, p.q_out_row_stride, p.q_out_head_stride)
+         if p.q_out_row_stride or p.q_out_head_stride else _arg("out", out, d, dt, nq))
     k = ko = None
     if key is not None:
         if key_out is None:
             key_out = _Alloc(stream, query.device).output(rows, p.N2, D, dtype=dt)
-        k = arg("key", key, p.N2, p.k_row_stride, p.k_head_stride)
-        ko = arg("key_out", key_out, p.N2, p.k_out_row_stride, p.k_out_head_stride)
+        nk = rows * p.N2 * D
+        k = (_heads("key", key, d, dt, p, p.N2, p.k_row_stride, p.k_head_stride) if p.k_row_stride or p.k_head_stride
+             else _arg("key", key, d, dt, nk))
+        ko = (_heads("key_out", key_out, d, dt, p, p.N2, p.k_out_row_stride, p.k_out_head_stride)
+              if p.k_out_row_stride or p.k_out_head_stride else _arg("key_out", key_out, d, dt, nk))
     _launch(d, lib().li_rope, ctypes.byref(p), _arg("positions", positions, d, torch.int32, rows),
             _arg("inv_freq", inv_freq, d, torch.float64, p.rot_dim // 2), q, k, o, ko, stream=stream)
     return out, key_out
