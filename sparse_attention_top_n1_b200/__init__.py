@@ -216,8 +216,9 @@ class _Alloc:
         if stream is None or device.type != "cuda":
             return
         on = stream
-        if not hasattr(stream, "cuda_stream"):             # a raw handle; 0 is the default stream
-            on = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
+        if not hasattr(stream, "cuda_stream"):             # a raw handle; 0 and 1 name the default stream
+            h = int(getattr(stream, "value", stream) or 0)
+            on = torch.cuda.ExternalStream(h, device=device) if h > 1 else torch.cuda.default_stream(device)
         reader = torch.cuda.current_stream(device)
         if on.cuda_stream != reader.cuda_stream:
             self.on, self.reader = on, reader

@@ -2,6 +2,7 @@
 and memory for a call on another stream belongs to that stream."""
 from __future__ import annotations
 
+import ctypes
 import weakref
 
 import numpy as np
@@ -153,3 +154,15 @@ def test_the_default_stream_by_its_handle():
         got = f(stream=0)
         torch.cuda.synchronize()
     assert all(torch.equal(a.cpu(), b) for a, b in zip(got, want))
+
+
+@pytest.mark.gpu
+def test_handles_of_every_kind():
+    f, want = _pages("reserve")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for h in (None, 0, 1, 2, ctypes.c_void_p(0), ctypes.c_void_p(side.cuda_stream), side.cuda_stream, side,
+              torch.cuda.default_stream()):
+        got = f(stream=h)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a.cpu(), b) for a, b in zip(got, want))
